@@ -173,7 +173,8 @@ def _round_bf16(y):
 def _quant(y):
     """One scale per row, and the nearest codes (the quotient in 64 bits: values lie next to a border)."""
     amax = y.abs().amax(dim=1).float()
-    s = torch.where(torch.isfinite(amax), amax / 127, math.nan)
+    s = torch.where(torch.isfinite(amax), amax / torch.full_like(amax, 127), math.nan)   # a division: by the
+    # number 127 torch multiplies with its rounded reciprocal
     q = torch.round(y.double() / s.double()[:, None])
     q = torch.where((s > 0)[:, None], q, 0.0).clamp(-127, 127).to(torch.int8)
     return q, s
@@ -256,7 +257,7 @@ def work(case):
 def _exact_codes(y):
     """Scale and codes of rows that hold bf16, fp16 or fp32 values, from the definition."""
     top = y.abs().max(dim=1, keepdim=True).values
-    scale = top / 127
+    scale = torch.div(top, torch.full_like(top, 127))
     held = scale.float().double()      # the scale is a 32-bit number, the codes go by that number
     return torch.round(y / held).to(torch.int8), scale[:, 0]
 
