@@ -238,6 +238,82 @@ size_t vitq_patch_embed_workspace_bytes(int n_tokens);
 #define VITQ_PATCH_DIM 1536
 #define VITQ_POS_GRID 48
 
+/* ------------------------------------------------------- INT8 path and rotary axes */
+
+/* Element types of the entry points below that take one.  With no rows (M or
+ * n_tokens 0) these entry points return VITQ_OK and launch nothing, and the pointers
+ * of the row matrices may be NULL. */
+#define VITQ_BF16 0
+#define VITQ_FP16 1
+#define VITQ_FP32 2
+
+/* INT8 codes with one scale per row (no counterpart in the sources, which quantise
+ * to FP8 in 128-column blocks: vit_quant_act).  A row is a token of an activation,
+ * or an output channel of a weight [N, K].  For each row
+ *   s = fl32(amax / 127),  q = round_half_even(x / s)  (the exact quotient by the
+ * fp32 number s), so codes lie in [-127, 127].  A zero scale gives zero codes; a
+ * row holding an infinity or a NaN gets s = NaN and zero codes, so its row of
+ * int8_gemm comes out NaN.  x: dtype [M, ldx] (first K columns used; any ldx >= K,
+ * any alignment of the type; rows 16-byte aligned take the fast path).  q: int8
+ * [M, ldq], ldq % 16 == 0, ldq >= K (columns from K on are left as they were).
+ * s: fp32 [M].  K <= VITQ_MAX_DIM. */
+int vit_quant_int8(const void* x, int dtype, int M, int K, int ldx, int8_t* q, int ldq, float* s, void* stream);
+
+/* LayerNorm with the bf16 result quantised as in vit_quant_int8 (no counterpart in
+ * the sources; the LayerNorm is vit_ln_quant's: statistics and affine step in fp64,
+ * one rounding to bf16).  x: bf16 [M, ldx]; gamma, beta bf16 [K]; eps >= 0. */
+int vit_ln_quant_int8(const void* x, int M, int K, int ldx, const void* gamma, const void* beta, float eps,
+                      int8_t* q, int ldq, float* s, void* stream);
+
+/* GELU(tanh) of a bf16 activation, rounded to bf16 (vit_gelu_quant's table) and
+ * quantised as in vit_quant_int8 (no counterpart in the sources).  f: bf16 [M, ldf]. */
+int vit_gelu_quant_int8(const void* f, int M, int K, int ldf, int8_t* q, int ldq, float* s, void* stream);
+
+/* INT8 W8A8 GEMM with a scale per token and per output channel (no counterpart in
+ * the sources; fp8_block_gemm is the FP8 block-128 one):
+ *   C[m,n] = dtype( sA[m] * sW[n] * sum_k A[m,k] W[n,k] + bias[n] + residual[m,n] )
+ * The sum is exact (32-bit integers), the rest fp32, one rounding to dtype.
+ * A: int8 [M, lda]; W: int8 [N, ldw]; lda and ldw % 16 == 0, A and W 16-byte
+ * aligned, any K <= VITQ_MAX_DIM (what lies behind column K of a row is not used).
+ * sA fp32 [M]; sW fp32 [N]; bias dtype [N] or NULL; residual dtype [M, ldr] or
+ * NULL (may be C itself, with ldr == ldc); C dtype [M, ldc].  Any N, ldc, ldr and
+ * alignment of the type; C and residual rows that are 16-byte aligned take the fast
+ * path. */
+int int8_gemm(const int8_t* A, int lda, const float* sA, const int8_t* W, int ldw, const float* sW, const void* bias,
+              const void* residual, int ldr, void* C, int ldc, int dtype, int M, int N, int K, void* stream);
+
+#define VITQ_ROPE_MAX_AXES 4
+#define VITQ_ROPE_INTERLEAVED 1 /* pair j on axis j % n_axes while that axis has pairs left, else on axis 0 */
+#define VITQ_ROPE_AXIS_FREQ 2   /* frequencies start over on each axis: theta^(-i / sections[a]), i-th pair of axis a */
+#define VITQ_ROPE_ADJACENT 4    /* pairs (2j, 2j+1) instead of (j, j + pairs) */
+#define VITQ_ROPE_INVERSE 8     /* turn back (by -angle): the gradient of the rotary */
+
+/* Layout of vit_rope_axes (host struct; strides in elements, all >= 0; the innermost
+ * dimension of a head is dense). */
+typedef struct {
+  int32_t dtype;                      /* VITQ_BF16, VITQ_FP16 or VITQ_FP32, q and k alike */
+  int32_t n_axes;                     /* 1 .. VITQ_ROPE_MAX_AXES */
+  int32_t sections[VITQ_ROPE_MAX_AXES]; /* rotary pairs of each axis; pairs = their sum */
+  int32_t heads_q, heads_k, head_dim; /* 2 * pairs <= head_dim <= 512; the rest of a head passes through */
+  int32_t flags;                      /* VITQ_ROPE_* */
+  double theta;
+  int64_t q_token, q_head, q_out_token, q_out_head;
+  int64_t k_token, k_head, k_out_token, k_out_head;
+  int64_t pos_token, pos_axis;        /* position of token t on axis a: pos[t * pos_token + a * pos_axis] */
+} vitq_rope_axes;
+
+/* Rotary over several position axes, e.g. (time, row, column) of a video's patches or
+ * of a language layer's image tokens (no counterpart in the sources for more than the two
+ * axes and the layout of vit_rope2d, [FRT] s3).  Pair j of a head turns by
+ * pos[axis(j)] * f_j, f_j = theta^(-j / pairs) (or per axis, see the flags); sections
+ * are laid out one after the other, or interleaved.  Angles in fp64, the rest in fp32,
+ * one rounding.  q: [n_tokens, heads_q, head_dim], k: [n_tokens, heads_k, head_dim] by
+ * the strides of p; q_out and k_out are either the inputs themselves (same pointer and
+ * strides) or share no element with any input.  heads_q or heads_k may be 0 (pointers
+ * unused).  pos: int32, may be negative. */
+int vit_rope_axes(const vitq_rope_axes* p, const void* q, void* q_out, const void* k, void* k_out,
+                  const int32_t* pos, int n_tokens, void* stream);
+
 /* ---------------------------------------------------------------- layers */
 
 /* One ViT block in place on x bf16 [n_tokens, 1152] ([FRT] s3 per-block chain):

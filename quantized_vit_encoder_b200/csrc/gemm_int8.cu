@@ -1,0 +1,351 @@
+// INT8 GEMM on the sm_100a tensor cores (tcgen05 kind::i8 + TMEM + TMA).
+//
+//   C[m, n] = T( sA[m] sW[n] sum_k A[m, k] W[n, k] + bias[n] + R[m, n] )
+//
+// One scale per token and per output channel: nothing changes along K, so the
+// whole sum stays in TMEM as exact 32-bit integers (K <= 2^16 and |code| <= 128
+// keep it below 2^31) and the scales are applied once per output, in fp32, before
+// the one rounding to T.
+#include "internal.h"
+#include "ptx.cuh"
+
+#include <cuda_fp16.h>
+
+namespace vitq {
+namespace {
+
+struct I8Args {
+  const float* sA;
+  const float* sW;
+  const void* bias;
+  const void* residual;
+  void* C;
+  int ldr, ldc, M, N, K;
+  int c_tma;     // C can be written by TMA (16-byte aligned base and row pitch)
+  int r_vec;     // residual can be read 16 bytes at a time
+};
+
+// ------------------------------------------------------------------ output types
+template <class T> __device__ __forceinline__ float to_f32(T v);
+template <> __device__ __forceinline__ float to_f32(float v) { return v; }
+template <> __device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+template <> __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <class T> __device__ __forceinline__ T of_f32(float v);
+template <> __device__ __forceinline__ float of_f32(float v) { return v; }
+template <> __device__ __forceinline__ __half of_f32(float v) { return __float2half_rn(v); }
+template <> __device__ __forceinline__ __nv_bfloat16 of_f32(float v) { return __float2bfloat16_rn(v); }
+
+// 16 bytes of T -> fp32 and back.
+template <class T>
+__device__ __forceinline__ void unpack16(const uint4& u, float* v) {
+  const T* p = reinterpret_cast<const T*>(&u);
+#pragma unroll
+  for (int i = 0; i < (int)(16 / sizeof(T)); ++i) v[i] = to_f32<T>(p[i]);
+}
+template <class T>
+__device__ __forceinline__ uint4 pack16(const float* v) {
+  uint4 u;
+  T* p = reinterpret_cast<T*>(&u);
+#pragma unroll
+  for (int i = 0; i < (int)(16 / sizeof(T)); ++i) p[i] = of_f32<T>(v[i]);
+  return u;
+}
+
+// ------------------------------------------------------------------ tiles
+template <int BN>
+struct I8Cfg {
+  static constexpr int BM = 128, BK = 128;   // 128 codes = one 128B swizzle row
+  static constexpr int STAGES = BN == 256 ? 3 : 5;
+  static constexpr int A_BYTES = BM * BK;
+  static constexpr int B_BYTES = BN * BK;
+  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+  static constexpr int NACC = 2;              // TMEM accumulators, alternating between tiles
+  static constexpr int EPI_WARPS = 4, EPI_WARP0 = 4;
+  static constexpr int THREADS = 256;
+  static constexpr int BOX_BYTES = 4096;      // 32 rows x 128 bytes of C
+  static constexpr int BOXES = 2;             // per epilogue warp
+  static constexpr int OUT_BYTES = EPI_WARPS * BOXES * BOX_BYTES;
+  static constexpr int COL_BYTES = EPI_WARPS * BN * 8;   // (sW, bias) per column, a copy per warp
+  static constexpr int BAR_BYTES = (2 * STAGES + 2 * NACC) * 8 + 16;
+  static constexpr size_t SMEM = (size_t)STAGES * STAGE_BYTES + OUT_BYTES + COL_BYTES + 1024 + BAR_BYTES;
+};
+
+template <int BN>
+struct I8Smem {
+  using Cfg = I8Cfg<BN>;
+  uint8_t* base;
+  __device__ uint32_t a(int s) const { return smem_u32(base + (size_t)s * Cfg::STAGE_BYTES); }
+  __device__ uint32_t b(int s) const { return a(s) + Cfg::A_BYTES; }
+  __device__ uint8_t* out(int w) const {
+    return base + (size_t)Cfg::STAGES * Cfg::STAGE_BYTES + (size_t)w * Cfg::BOXES * Cfg::BOX_BYTES;
+  }
+  __device__ float2* cols(int w) const {
+    return reinterpret_cast<float2*>(base + (size_t)Cfg::STAGES * Cfg::STAGE_BYTES + Cfg::OUT_BYTES) + w * BN;
+  }
+  __device__ uint64_t* bars() const {
+    return reinterpret_cast<uint64_t*>(base + (size_t)Cfg::STAGES * Cfg::STAGE_BYTES + Cfg::OUT_BYTES + Cfg::COL_BYTES);
+  }
+  __device__ uint32_t full(int s) const { return smem_u32(bars() + s); }
+  __device__ uint32_t empty(int s) const { return smem_u32(bars() + Cfg::STAGES + s); }
+  __device__ uint32_t tfull(int b) const { return smem_u32(bars() + 2 * Cfg::STAGES + b); }
+  __device__ uint32_t tempty(int b) const { return smem_u32(bars() + 2 * Cfg::STAGES + Cfg::NACC + b); }
+  __device__ uint32_t* tmem_holder() const {
+    return reinterpret_cast<uint32_t*>(bars() + 2 * Cfg::STAGES + 2 * Cfg::NACC);
+  }
+  __device__ volatile int* abort_flag() const { return reinterpret_cast<volatile int*>(tmem_holder() + 1); }
+};
+
+// Tile order of the other GEMMs: CTAs that run together read different W tiles.
+__device__ __forceinline__ void i8_tile_coords(int tile, int tiles_m, int tiles_n, int& m, int& n) {
+  m = tile % tiles_m;
+  n = (tile / tiles_m + m) % tiles_n;
+}
+
+template <int BN>
+__device__ void i8_producer(const I8Smem<BN>& sm, const CUtensorMap* tmA, const CUtensorMap* tmB, int tiles_m,
+                            int tiles_n, int num_tiles, int nkb) {
+  using Cfg = I8Cfg<BN>;
+  int stage = 0;
+  uint32_t phase = 0;
+  for (int tile = blockIdx.x; tile < num_tiles; tile += gridDim.x) {
+    int mt, nt;
+    i8_tile_coords(tile, tiles_m, tiles_n, mt, nt);
+    for (int kb = 0; kb < nkb; ++kb) {
+      if (!mbar_wait(sm.empty(stage), phase ^ 1u, sm.abort_flag())) return;
+      mbar_arrive_expect_tx(sm.full(stage), Cfg::STAGE_BYTES);
+      tma_load_2d(sm.a(stage), tmA, kb * Cfg::BK, mt * Cfg::BM, sm.full(stage));
+      tma_load_2d(sm.b(stage), tmB, kb * Cfg::BK, nt * BN, sm.full(stage));
+      if (++stage == Cfg::STAGES) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    }
+  }
+}
+
+template <int BN>
+__device__ void i8_mma(const I8Smem<BN>& sm, uint32_t tmem_base, int num_tiles, int nkb, int K) {
+  using Cfg = I8Cfg<BN>;
+  constexpr uint32_t idesc = make_idesc_i8(128, BN);
+  int stage = 0;
+  uint32_t phase = 0, it = 0;
+  for (int tile = blockIdx.x; tile < num_tiles; tile += gridDim.x, ++it) {
+    const uint32_t acc = it % Cfg::NACC;
+    if (!mbar_wait(sm.tempty(acc), ((it / Cfg::NACC) & 1u) ^ 1u, sm.abort_flag())) return;
+    tc_fence_after();
+    for (int kb = 0; kb < nkb; ++kb) {
+      if (!mbar_wait(sm.full(stage), phase, sm.abort_flag())) return;
+      tc_fence_after();
+      const uint32_t a0 = sm.a(stage), b0 = sm.b(stage);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)   // 32 codes each; steps that lie past K hold zeros and are left out
+        if (kb * Cfg::BK + 32 * k < K)
+          mma_i8_ss(tmem_base + acc * BN, make_smem_desc(a0 + 32 * k, 16, 1024, kSwizzle128B),
+                    make_smem_desc(b0 + 32 * k, 16, 1024, kSwizzle128B), idesc, (kb > 0 || k > 0) ? 1u : 0u);
+      tc_commit(sm.empty(stage));
+      if (++stage == Cfg::STAGES) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    }
+    tc_commit(sm.tfull(acc));
+  }
+}
+
+template <int BN, class T>
+__device__ void i8_epilogue(const I8Smem<BN>& sm, uint32_t tmem_base, const I8Args& g, const CUtensorMap* tmC,
+                            int tiles_m, int tiles_n, int num_tiles) {
+  using Cfg = I8Cfg<BN>;
+  constexpr int PER = 16 / (int)sizeof(T);          // elements per 16 bytes
+  constexpr int BOXC = 128 / (int)sizeof(T);        // columns per box
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int ew = warp - Cfg::EPI_WARP0, quad = warp & 3;
+  uint8_t* stg = sm.out(ew);
+  float2* cols = sm.cols(ew);
+  const T* bias = reinterpret_cast<const T*>(g.bias);
+  const T* res = reinterpret_cast<const T*>(g.residual);
+  uint32_t it = 0, box = 0;
+  for (int tile = blockIdx.x; tile < num_tiles; tile += gridDim.x, ++it) {
+    int mt, nt;
+    i8_tile_coords(tile, tiles_m, tiles_n, mt, nt);
+    const int col0 = nt * BN, y0 = mt * Cfg::BM + quad * 32, row = y0 + lane;
+    const uint32_t acc = it % Cfg::NACC;
+    __syncwarp();
+    for (int c = lane; c < BN; c += 32) {
+      const int n = col0 + c;
+      cols[c] = n < g.N ? make_float2(__ldg(g.sW + n), bias ? to_f32<T>(bias[n]) : 0.f) : make_float2(0.f, 0.f);
+    }
+    const float sa = row < g.M ? __ldg(g.sA + row) : 0.f;
+    __syncwarp();
+    const bool ok = mbar_wait(sm.tfull(acc), (it / Cfg::NACC) & 1u, sm.abort_flag());
+    if (!__all_sync(0xffffffffu, ok)) return;
+    tc_fence_after();
+    const uint32_t taddr = tmem_base + ((uint32_t)(quad * 32) << 16) + acc * BN;
+#pragma unroll 1
+    for (int c0 = 0; c0 < BN; c0 += BOXC) {
+      if (col0 + c0 >= g.N) break;
+      uint8_t* slot = stg + (box & 1u) * Cfg::BOX_BYTES;
+      if (g.c_tma) {   // the store before last has read its box
+        if (lane == 0) bulk_wait_read<1>();
+        __syncwarp();
+      }
+#pragma unroll
+      for (int h = 0; h < BOXC; h += 32) {
+        uint32_t r[32];
+        tmem_ld32(taddr + c0 + h, r);
+        uint4 ru[32 / PER];
+        const int colb = col0 + c0 + h;
+        if (res) {
+#pragma unroll
+          for (int c = 0; c < 32 / PER; ++c) {
+            const int col = colb + c * PER;
+            ru[c] = make_uint4(0u, 0u, 0u, 0u);
+            if (row < g.M) {
+              const T* p = res + (size_t)row * g.ldr + col;
+              if (g.r_vec && col + PER <= g.N) {
+                ru[c] = *reinterpret_cast<const uint4*>(p);
+              } else {
+#pragma unroll
+                for (int i = 0; i < PER; ++i)
+                  if (col + i < g.N) reinterpret_cast<T*>(&ru[c])[i] = p[i];
+              }
+            }
+          }
+        }
+        tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < 32 / PER; ++c) {
+          float v[PER];
+#pragma unroll
+          for (int i = 0; i < PER; ++i) {
+            const float2 sb = cols[c0 + h + c * PER + i];
+            v[i] = __fmaf_rn(__int2float_rn((int)r[c * PER + i]) * sa, sb.x, sb.y);
+          }
+          if (res) {
+            float rv[PER];
+            unpack16<T>(ru[c], rv);
+#pragma unroll
+            for (int i = 0; i < PER; ++i) v[i] += rv[i];
+          }
+          if (g.c_tma) {
+            const int ch = (h * (int)sizeof(T)) / 16 + c;
+            *reinterpret_cast<uint4*>(slot + lane * 128 + ((ch ^ (lane & 7)) << 4)) = pack16<T>(v);
+          } else if (row < g.M) {
+            T* p = reinterpret_cast<T*>(g.C) + (size_t)row * g.ldc + colb + c * PER;
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+              if (colb + c * PER + i < g.N) p[i] = of_f32<T>(v[i]);
+          }
+        }
+      }
+      if (g.c_tma) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if (y0 < g.M) tma_store_2d(tmC, smem_u32(slot), col0 + c0, y0);
+          bulk_commit_group();
+        }
+        ++box;
+      }
+    }
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(sm.tempty(acc));
+  }
+  if (lane == 0) bulk_wait_all();
+}
+
+template <int BN, class T>
+__global__ void __launch_bounds__(I8Cfg<BN>::THREADS, 1)
+    int8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                     const __grid_constant__ CUtensorMap tmC, const I8Args args) {
+  using Cfg = I8Cfg<BN>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  pdl_trigger();
+  I8Smem<BN> sm;
+  sm.base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int nkb = (args.K + Cfg::BK - 1) / Cfg::BK;
+  const int tiles_m = (args.M + Cfg::BM - 1) / Cfg::BM;
+  const int tiles_n = (args.N + BN - 1) / BN;
+  const int num_tiles = tiles_m * tiles_n;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < Cfg::STAGES; ++s) {
+      mbar_init(sm.full(s), 1);
+      mbar_init(sm.empty(s), 1);
+    }
+    for (int b = 0; b < Cfg::NACC; ++b) {
+      mbar_init(sm.tfull(b), 1);
+      mbar_init(sm.tempty(b), Cfg::EPI_WARPS);
+    }
+    *sm.abort_flag() = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(sm.tmem_holder()), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  pdl_wait();   // inputs may be the previous kernel's outputs
+  const uint32_t tmem_base = *sm.tmem_holder();
+  if (warp < Cfg::EPI_WARP0) {
+    if (warp == 0 && lane == 0) {
+      i8_producer<BN>(sm, &tmA, &tmB, tiles_m, tiles_n, num_tiles, nkb);
+    } else if (warp == 1 && lane == 0) {
+      i8_mma<BN>(sm, tmem_base, num_tiles, nkb, args.K);
+    }
+  } else {
+    i8_epilogue<BN, T>(sm, tmem_base, args, &tmC, tiles_m, tiles_n, num_tiles);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (*sm.abort_flag()) settle_pause(50000);
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem_base, 512);
+  }
+}
+
+template <int BN, class T>
+cudaError_t i8_launch(const Int8Gemm& p, int num_sms, cudaStream_t st) {
+  using Cfg = I8Cfg<BN>;
+  constexpr int es = (int)sizeof(T);
+  I8Args a{p.sA, p.sW, p.bias, p.residual, p.C, p.ldr, p.ldc, p.M, p.N, p.K, 0, 0};
+  a.c_tma = (reinterpret_cast<uintptr_t>(p.C) & 15u) == 0 && ((size_t)p.ldc * es) % 16 == 0;
+  a.r_vec = (reinterpret_cast<uintptr_t>(p.residual) & 15u) == 0 && ((size_t)p.ldr * es) % 16 == 0;
+  CUtensorMap tmA, tmB, tmC;
+  cudaError_t e = encode_tma_2d_ld(&tmA, 1, p.A, p.K, p.M, (size_t)p.lda, 128, 128);
+  if (e != cudaSuccess) return e;
+  e = encode_tma_2d_ld(&tmB, 1, p.W, p.K, p.N, (size_t)p.ldw, 128, BN);
+  if (e != cudaSuccess) return e;
+  if (a.c_tma) {
+    e = encode_tma_2d_ld(&tmC, es, p.C, p.N, p.M, (size_t)p.ldc * es, 128 / es, 32);
+    if (e != cudaSuccess) return e;
+  } else {
+    tmC = tmA;   // not used
+  }
+  e = cudaFuncSetAttribute(int8_gemm_kernel<BN, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg::SMEM);
+  if (e != cudaSuccess) return e;
+  const long long tiles = (long long)((p.M + Cfg::BM - 1) / Cfg::BM) * ((p.N + BN - 1) / BN);
+  const int grid = tiles < num_sms ? (int)tiles : num_sms;
+  return launch_pdl(int8_gemm_kernel<BN, T>, dim3(grid), dim3(Cfg::THREADS), Cfg::SMEM, st, tmA, tmB, tmC, a);
+}
+
+template <class T>
+cudaError_t i8_pick(const Int8Gemm& p, int num_sms, cudaStream_t st) {
+  return p.N > 128 ? i8_launch<256, T>(p, num_sms, st) : i8_launch<128, T>(p, num_sms, st);
+}
+
+}  // namespace
+
+cudaError_t launch_int8_gemm(const Int8Gemm& p, int num_sms, cudaStream_t st) {
+  if (p.M == 0) return cudaSuccess;
+  if (p.dtype == 0) return i8_pick<__nv_bfloat16>(p, num_sms, st);
+  if (p.dtype == 1) return i8_pick<__half>(p, num_sms, st);
+  return i8_pick<float>(p, num_sms, st);
+}
+
+}  // namespace vitq

@@ -55,6 +55,10 @@ cudaError_t encode_tma_2d_u8(CUtensorMap* tm, const void* base, int cols, int ro
 // (box_cols = 64).
 cudaError_t encode_tma_2d_bf16(CUtensorMap* tm, const void* base, int cols, int rows, int box_cols,
                                int box_rows);
+// 2D matrix [rows, cols] of 1-, 2- or 4-byte elements with a row pitch in bytes (a multiple of 16), 128B swizzle
+// (box_cols * elem_bytes = 128).
+cudaError_t encode_tma_2d_ld(CUtensorMap* tm, int elem_bytes, const void* base, int cols, int rows, size_t pitch,
+                             int box_cols, int box_rows);
 // Packed qkv [n, 3, 16, 72] bf16 viewed as 3D (d = 72, slot = 48, token = n); box {box_d, 1, 128}.
 // lo = true: 128B swizzle (box_d = 64); lo = false: 32B swizzle (box_d = 16).
 cudaError_t encode_tma_qkv(CUtensorMap* tm, const void* qkv, int n_tokens, int box_d, bool lo);
@@ -92,6 +96,53 @@ cudaError_t launch_bf16_gemm(const __nv_bfloat16* A, const __nv_bfloat16* W, con
                              int num_sms, cudaStream_t st);
 cudaError_t launch_attention(const __nv_bfloat16* qkv, int n_tokens, const int32_t* cu, int n_seqs,
                              int max_seqlen, float scale, bool v_f16, __nv_bfloat16* out, cudaStream_t st);
+
+// INT8 rows (quant_int8.cu): x [M, K] of row stride ldx -> codes q [M, K] of row stride ldq, one scale per row.
+struct RowsInt8 {
+  const void* x;
+  int ldx, M, K;
+  const __nv_bfloat16 *gamma, *beta;   // LayerNorm only
+  double eps;
+  int8_t* q;
+  int ldq;
+  float* s;
+};
+cudaError_t launch_quant_int8(const RowsInt8& a, int dtype, cudaStream_t st);
+cudaError_t launch_ln_quant_int8(const RowsInt8& a, cudaStream_t st);
+cudaError_t launch_gelu_quant_int8(const RowsInt8& a, cudaStream_t st);
+
+// INT8 GEMM (gemm_int8.cu); dtype as VITQ_BF16 / VITQ_FP16 / VITQ_FP32 (bias, residual and C).
+struct Int8Gemm {
+  const int8_t* A;
+  int lda;
+  const float* sA;
+  const int8_t* W;
+  int ldw;
+  const float* sW;
+  const void *bias, *residual;
+  int ldr;
+  void* C;
+  int ldc, dtype, M, N, K;
+};
+cudaError_t launch_int8_gemm(const Int8Gemm& p, int num_sms, cudaStream_t st);
+
+// Rotary over several axes (rope_axes.cu).  Strides in elements.
+constexpr int kRopeMaxPairs = 256;
+struct RopeSide {
+  const void* x;
+  void* y;
+  long long xt, xh, yt, yh;   // token and head strides of input and output
+  int heads;
+};
+struct RopeAxes {
+  RopeSide side[2];             // q, k
+  const int32_t* pos;
+  long long pos_t, pos_a;
+  int n, d, pairs, inverse, adjacent;
+  double turns[kRopeMaxPairs];   // turns (angle / 2 pi) per position step
+  uint8_t axis[kRopeMaxPairs];
+};
+cudaError_t launch_rope_axes(const RopeAxes& p, int dtype, cudaStream_t st);
 
 cudaError_t launch_selftest_wait(int limit_us, cudaStream_t st);
 

@@ -68,6 +68,15 @@ class TowerWeightsMixed(C.Structure):
                 ("mergers", MergerWeightsBf16 * 4)]
 
 
+class RopeAxes(C.Structure):
+    """vitq_rope_axes: types, sections and strides of a several-axis rotary call."""
+    _fields_ = ([("dtype", C.c_int32), ("n_axes", C.c_int32), ("sections", C.c_int32 * 4),
+                 ("heads_q", C.c_int32), ("heads_k", C.c_int32), ("head_dim", C.c_int32), ("flags", C.c_int32),
+                 ("theta", C.c_double)] +
+                [(n, C.c_int64) for n in ("q_token", "q_head", "q_out_token", "q_out_head", "k_token", "k_head",
+                                          "k_out_token", "k_out_head", "pos_token", "pos_axis")])
+
+
 _SIGS = {
     "vit_quant_act": [_vp, _i, _i, _i, _vp, _vp, _i, _vp],
     "vit_quant_weight": [_vp, _i, _i, _vp, _vp, _vp],
@@ -79,6 +88,11 @@ _SIGS = {
     "vit_rope2d": [_vp, _i, _vp, _i, _vp],
     "vit_positions": [_vp, _i, _vp, _vp, _vp],
     "vit_attention_varlen": [_vp, _i, _vp, _i, _i, _f, _i, _vp, _vp],
+    "vit_quant_int8": [_vp, _i, _i, _i, _i, _vp, _i, _vp, _vp],
+    "vit_ln_quant_int8": [_vp, _i, _i, _i, _vp, _vp, _f, _vp, _i, _vp, _vp],
+    "vit_gelu_quant_int8": [_vp, _i, _i, _i, _vp, _i, _vp, _vp],
+    "int8_gemm": [_vp, _i, _vp, _vp, _i, _vp, _vp, _vp, _i, _vp, _i, _i, _i, _i, _i, _vp],
+    "vit_rope_axes": [C.POINTER(RopeAxes), _vp, _vp, _vp, _vp, _vp, _i, _vp],
     "vit_block_forward": [C.POINTER(BlockWeights), _vp, _i, _vp, _i, _i, _vp, _vp, _sz, _vp],
     "vitq_block_workspace_bytes": [_i],
     "vit_merger_forward": [C.POINTER(MergerWeights), _vp, _i, _vp, _vp, _sz, _vp],
@@ -345,6 +359,183 @@ def attention_varlen(qkv, cu_seqlens, max_seqlen: int, scale: float | None = Non
     _check(load().vit_attention_varlen(_p(qkv), n, _p(cu_seqlens), cu_seqlens.shape[0] - 1, max_seqlen, scale,
                                        flags, _p(out), _stream(stream)), "vit_attention_varlen")
     return out
+
+
+# ------------------------------------------------------- INT8 path and rotary axes
+
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}   # VITQ_BF16, VITQ_FP16, VITQ_FP32
+
+
+def _on_current(*tensors):
+    """The library launches on the current device: every tensor has to live there."""
+    if _DEVICE_TYPE == "cuda":
+        cur = torch.cuda.current_device()
+        for t in tensors:
+            if t is not None and t.device.index != cur:
+                raise VitqError(f"tensor on {t.device}, current device is cuda:{cur}")
+
+
+def _mat(t, name, dtypes, cols=None, rows=None):
+    """Check a matrix with dense rows; its row stride (for one row, the padded width)."""
+    if not isinstance(t, torch.Tensor):
+        raise VitqError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+    if t.device.type != _DEVICE_TYPE:
+        raise VitqError(f"{name}: tensor on {t.device}; the library reads device memory only")
+    if t.dtype not in dtypes:
+        raise VitqError(f"{name}: dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
+    if t.dim() != 2 or (cols is not None and t.shape[1] != cols) or (rows is not None and t.shape[0] != rows):
+        raise VitqError(f"{name}: shape {tuple(t.shape)}, expected {(rows, cols)}")
+    m, k = t.shape
+    ld, inner = t.stride()
+    if m <= 1:
+        ld = (k + 15) // 16 * 16
+    if (inner != 1 and k > 1) or ld < k:
+        raise VitqError(f"{name}: strides {t.stride()} are not a dense row layout")
+    return ld
+
+
+def _new(shape, dtype, like, stream):
+    """An output tensor, allocated for the stream that the kernel runs on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _codes_out(out, x, M, K, stream):
+    """The (codes, scales) to write: given, or new ones with a row stride of a multiple of 16."""
+    if out is None:
+        q = _new((M, (K + 15) // 16 * 16), torch.int8, x, stream)
+        return (q if q.shape[1] == K else q[:, :K]), _new((M,), _f32, x, stream), q.shape[1]
+    q, s = out
+    ldq = _mat(q, "out codes", (torch.int8,), K, M)
+    _arg(s, "out scales", _f32, (M,))
+    _on_current(q, s)
+    return q, s, ldq
+
+
+def quant_int8(x, out=None, stream=None):
+    """INT8 codes and one scale per row of bf16, fp16 or fp32 x [M, K] (tokens, or a weight's output channels)
+    -> (codes int8 [M, K] with a row stride of a multiple of 16, scales fp32 [M])."""
+    ldx = _mat(x, "x", _DTYPES)
+    M, K = x.shape
+    _on_current(x)
+    q, s, ldq = _codes_out(out, x, M, K, stream)
+    _check(load().vit_quant_int8(_p(x), _DTYPES[x.dtype], M, K, ldx, _p(q), ldq, _p(s), _stream(stream)),
+           "vit_quant_int8")
+    return q, s
+
+
+def ln_quant_int8(x, gamma, beta, eps: float = 1e-6, out=None, stream=None):
+    """LayerNorm of bf16 x [M, K] (rows dense), rounded to bf16 and INT8-quantised per row -> (codes, scales)."""
+    ldx = _mat(x, "x", (_bf16,))
+    M, K = x.shape
+    _arg(gamma, "gamma", _bf16, (K,))
+    _arg(beta, "beta", _bf16, (K,))
+    _on_current(x, gamma, beta)
+    q, s, ldq = _codes_out(out, x, M, K, stream)
+    _check(load().vit_ln_quant_int8(_p(x), M, K, ldx, _p(gamma), _p(beta), eps, _p(q), ldq, _p(s), _stream(stream)),
+           "vit_ln_quant_int8")
+    return q, s
+
+
+def gelu_quant_int8(f, out=None, stream=None):
+    """GELU(tanh) of bf16 f [M, K] (rows dense), rounded to bf16 and INT8-quantised per row -> (codes, scales)."""
+    ldf = _mat(f, "f", (_bf16,))
+    M, K = f.shape
+    _on_current(f)
+    q, s, ldq = _codes_out(out, f, M, K, stream)
+    _check(load().vit_gelu_quant_int8(_p(f), M, K, ldf, _p(q), ldq, _p(s), _stream(stream)), "vit_gelu_quant_int8")
+    return q, s
+
+
+def int8_gemm(qa, sa, qw, sw, bias=None, residual=None, out=None, out_dtype=torch.bfloat16, stream=None):
+    """C [M, N] = sa[m] sw[n] (qa . qw^T) (+ bias) (+ residual) from int8 codes qa [M, K], qw [N, K] (row strides
+    of a multiple of 16) and fp32 scales sa [M], sw [N]; C, bias and residual bf16, fp16 or fp32 alike."""
+    lda = _mat(qa, "qa", (torch.int8,))
+    M, K = qa.shape
+    ldw = _mat(qw, "qw", (torch.int8,), K)
+    N = qw.shape[0]
+    _arg(sa, "sa", _f32, (M,))
+    _arg(sw, "sw", _f32, (N,))
+    if out is not None:
+        out_dtype = out.dtype
+    if out_dtype not in _DTYPES:
+        raise VitqError(f"out_dtype: {out_dtype}, expected bf16, fp16 or fp32")
+    t = (out_dtype,)
+    ldr = 0
+    if bias is not None:
+        _arg(bias, "bias", out_dtype, (N,))
+    if residual is not None:
+        ldr = _mat(residual, "residual", t, N, M)
+    _on_current(qa, sa, qw, sw, bias, residual, out)
+    if out is None:
+        out = _new((M, N), out_dtype, qa, stream)
+        ldc = N
+    else:
+        ldc = _mat(out, "out", t, N, M)
+    _check(load().int8_gemm(_p(qa), lda, _p(sa), _p(qw), ldw, _p(sw), _p(bias), _p(residual), ldr, _p(out), ldc,
+                            _DTYPES[out_dtype], M, N, K, _stream(stream)), "int8_gemm")
+    return out
+
+
+ROPE_INTERLEAVED, ROPE_AXIS_FREQ, ROPE_ADJACENT, ROPE_INVERSE = 1, 2, 4, 8
+
+
+def _heads(t, name, n=None, dtype=None, like=None):
+    """Check a [tokens, heads, head_dim] tensor with a dense innermost dimension."""
+    if not isinstance(t, torch.Tensor):
+        raise VitqError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+    if t.device.type != _DEVICE_TYPE:
+        raise VitqError(f"{name}: tensor on {t.device}; the library reads device memory only")
+    if t.dtype not in _DTYPES or (dtype is not None and t.dtype != dtype):
+        raise VitqError(f"{name}: dtype {t.dtype}, expected {dtype or 'bf16, fp16 or fp32'}")
+    if t.dim() != 3 or (n is not None and t.shape[0] != n) or (like is not None and t.shape != like.shape):
+        raise VitqError(f"{name}: shape {tuple(t.shape)}, expected {tuple(like.shape) if like is not None else 'three dims'}")
+    if t.shape[2] > 1 and t.stride(2) != 1:
+        raise VitqError(f"{name}: strides {t.stride()}, the innermost dimension must be dense")
+
+
+def rope_axes(q, k, pos, sections, theta: float = 10000.0, interleaved: bool = False, axis_freq: bool = False,
+              adjacent: bool = False, inverse: bool = False, out=None, stream=None):
+    """Rotary over several position axes of q [n, hq, d] and k [n, hk, d] (k may be None; any strides, the innermost
+    dense) with int32 positions pos [n, axes] and `sections` rotary pairs per axis -> (q', k'), new tensors or `out`.
+    inverse=True turns back: the gradient of the rotary.  See vit_rope_axes for the flags."""
+    _heads(q, "q")
+    n, hq, d = q.shape
+    hk = 0
+    if k is not None:
+        _heads(k, "k", n, q.dtype)
+        hk = k.shape[1]
+        if k.shape[2] != d:
+            raise VitqError(f"k: head dim {k.shape[2]}, q has {d}")
+    axes = len(sections)
+    if not 1 <= axes <= 4:
+        raise VitqError(f"sections: {axes} axes, expected 1 to 4")
+    if pos.device.type != _DEVICE_TYPE or pos.dtype != _i32 or tuple(pos.shape) != (n, axes):
+        raise VitqError(f"pos: {pos.dtype} {tuple(pos.shape)} on {pos.device}, expected int32 {(n, axes)} on the device")
+    _on_current(q, k, pos)
+    if out is None:
+        qo = _new((n, hq, d), q.dtype, q, stream)
+        ko = None if k is None else _new((n, hk, d), q.dtype, q, stream)
+    else:
+        qo, ko = out
+        _heads(qo, "out q", n, q.dtype, q)
+        if k is not None:
+            _heads(ko, "out k", n, q.dtype, k)
+        _on_current(qo, ko)
+    flags = (ROPE_INTERLEAVED * interleaved | ROPE_AXIS_FREQ * axis_freq | ROPE_ADJACENT * adjacent |
+             ROPE_INVERSE * inverse)
+    p = RopeAxes(_DTYPES[q.dtype], axes, (C.c_int32 * 4)(*sections), hq, hk, d, flags, theta, *q.stride()[:2],
+                 *qo.stride()[:2], *(k.stride()[:2] + ko.stride()[:2] if hk else (0, 0, 0, 0)), *pos.stride())
+    _check(load().vit_rope_axes(C.byref(p), _p(q), _p(qo), _p(k), _p(ko), _p(pos), n, _stream(stream)),
+           "vit_rope_axes")
+    return qo, ko
+
+
+def rope_axes_(q, k, pos, sections, **kw):
+    """rope_axes in place on q and k."""
+    return rope_axes(q, k, pos, sections, out=(q, k), **kw)
 
 
 # ---------------------------------------------------------------- layers
