@@ -9,6 +9,7 @@ from __future__ import annotations
 import ctypes as C
 import math
 import os
+import struct
 
 import torch
 
@@ -92,7 +93,7 @@ _SIGS = {
     "vit_ln_quant_int8": [_vp, _i, _i, _i, _vp, _vp, _f, _vp, _i, _vp, _vp],
     "vit_gelu_quant_int8": [_vp, _i, _i, _i, _vp, _i, _vp, _vp],
     "int8_gemm": [_vp, _i, _vp, _vp, _i, _vp, _vp, _vp, _i, _vp, _i, _i, _i, _i, _i, _vp],
-    "vit_rope_axes": [C.POINTER(RopeAxes), _vp, _vp, _vp, _vp, _vp, _i, _vp],
+    "vit_rope_axes": [_vp, _vp, _vp, _vp, _vp, _vp, _i, _vp],
     "vit_block_forward": [C.POINTER(BlockWeights), _vp, _i, _vp, _i, _i, _vp, _vp, _sz, _vp],
     "vitq_block_workspace_bytes": [_i],
     "vit_merger_forward": [C.POINTER(MergerWeights), _vp, _i, _vp, _vp, _sz, _vp],
@@ -364,136 +365,158 @@ def attention_varlen(qkv, cu_seqlens, max_seqlen: int, scale: float | None = Non
 # ------------------------------------------------------- INT8 path and rotary axes
 
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}   # VITQ_BF16, VITQ_FP16, VITQ_FP32
+_BF16_ONLY, _I8_ONLY, _F32_ONLY = (_bf16,), (torch.int8,), (_f32,)
+
+# The kernels behind these calls take a few microseconds at small sizes, so their checks read each property of a
+# tensor once and allocate with new_empty; a call that fails a check is explained by _why.
 
 
-def _on_current(*tensors):
-    """The library launches on the current device: every tensor has to live there."""
-    if _DEVICE_TYPE == "cuda":
-        cur = torch.cuda.current_device()
-        for t in tensors:
-            if t is not None and t.device.index != cur:
-                raise VitqError(f"tensor on {t.device}, current device is cuda:{cur}")
+def _device(t, name):
+    """Index of the current device, where the library launches and every tensor has to live (t: the first of them)."""
+    if _DEVICE_TYPE != "cuda":
+        return -1
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise _why(t, name, -1, (), (), "")
+    return torch.cuda.current_device()
 
 
-def _mat(t, name, dtypes, cols=None, rows=None):
-    """Check a matrix with dense rows; its row stride (for one row, the padded width)."""
+def _raw(stream, dev):
+    """The cudaStream_t of `stream`, or of the current one (by the call that builds no Stream object: 0.1 us, not 3)."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(dev) if dev >= 0 else None
+
+
+def _why(t, name, dev, dtypes, shape, dense):
+    """The VitqError for a tensor that failed a check."""
     if not isinstance(t, torch.Tensor):
-        raise VitqError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+        return VitqError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
     if t.device.type != _DEVICE_TYPE:
-        raise VitqError(f"{name}: tensor on {t.device}; the library reads device memory only")
+        return VitqError(f"{name}: tensor on {t.device}; the library reads device memory only")
+    if t.get_device() != dev:
+        return VitqError(f"{name}: tensor on {t.device}, current device is cuda:{dev}")
     if t.dtype not in dtypes:
-        raise VitqError(f"{name}: dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
-    if t.dim() != 2 or (cols is not None and t.shape[1] != cols) or (rows is not None and t.shape[0] != rows):
-        raise VitqError(f"{name}: shape {tuple(t.shape)}, expected {(rows, cols)}")
+        return VitqError(f"{name}: dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
+    if t.dim() != len(shape) or any(w is not None and w != d for w, d in zip(shape, t.shape)):
+        return VitqError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    return VitqError(f"{name}: strides {t.stride()}, expected {dense}")
+
+
+def _mat(t, name, dev, dtypes, rows=None, cols=None):
+    """Check a matrix with dense rows -> (rows, columns, row stride; for at most one row its padded width)."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype not in dtypes or t.dim() != 2:
+        raise _why(t, name, dev, dtypes, (rows, cols), "")
     m, k = t.shape
+    if (rows is not None and m != rows) or (cols is not None and k != cols):
+        raise _why(t, name, dev, dtypes, (rows, cols), "")
     ld, inner = t.stride()
     if m <= 1:
         ld = (k + 15) // 16 * 16
     if (inner != 1 and k > 1) or ld < k:
-        raise VitqError(f"{name}: strides {t.stride()} are not a dense row layout")
-    return ld
+        raise _why(t, name, dev, dtypes, (rows, cols), "dense rows")
+    return m, k, ld
 
 
-def _new(shape, dtype, like, stream):
+def _vec(t, name, dev, dtype, n):
+    """Check a dense vector of n elements -> its address."""
+    if (not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype is not dtype or t.dim() != 1
+            or t.shape[0] != n or not t.is_contiguous()):
+        raise _why(t, name, dev, (dtype,), (n,), "a dense vector")
+    return t.data_ptr()
+
+
+def _new(like, shape, dtype, stream):
     """An output tensor, allocated for the stream that the kernel runs on."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return like.new_empty(shape, dtype=dtype)
 
 
-def _codes_out(out, x, M, K, stream):
-    """The (codes, scales) to write: given, or new ones with a row stride of a multiple of 16."""
+def _codes_out(out, x, dev, m, k, stream):
+    """The (codes, scales, row stride) to write: given, or new ones with a row stride of a multiple of 16."""
     if out is None:
-        q = _new((M, (K + 15) // 16 * 16), torch.int8, x, stream)
-        return (q if q.shape[1] == K else q[:, :K]), _new((M,), _f32, x, stream), q.shape[1]
+        ldq = (k + 15) // 16 * 16
+        q = _new(x, (m, ldq), torch.int8, stream)
+        return (q if ldq == k else q[:, :k]), _new(x, (m,), _f32, stream), ldq
     q, s = out
-    ldq = _mat(q, "out codes", (torch.int8,), K, M)
-    _arg(s, "out scales", _f32, (M,))
-    _on_current(q, s)
+    ldq = _mat(q, "out codes", dev, _I8_ONLY, m, k)[2]
+    _vec(s, "out scales", dev, _f32, m)
     return q, s, ldq
 
 
 def quant_int8(x, out=None, stream=None):
     """INT8 codes and one scale per row of bf16, fp16 or fp32 x [M, K] (tokens, or a weight's output channels)
     -> (codes int8 [M, K] with a row stride of a multiple of 16, scales fp32 [M])."""
-    ldx = _mat(x, "x", _DTYPES)
-    M, K = x.shape
-    _on_current(x)
-    q, s, ldq = _codes_out(out, x, M, K, stream)
-    _check(load().vit_quant_int8(_p(x), _DTYPES[x.dtype], M, K, ldx, _p(q), ldq, _p(s), _stream(stream)),
-           "vit_quant_int8")
+    dev = _device(x, "x")
+    m, k, ldx = _mat(x, "x", dev, _DTYPES)
+    q, s, ldq = _codes_out(out, x, dev, m, k, stream)
+    _check(load().vit_quant_int8(x.data_ptr(), _DTYPES[x.dtype], m, k, ldx, q.data_ptr(), ldq, s.data_ptr(),
+                                 _raw(stream, dev)), "vit_quant_int8")
     return q, s
 
 
 def ln_quant_int8(x, gamma, beta, eps: float = 1e-6, out=None, stream=None):
     """LayerNorm of bf16 x [M, K] (rows dense), rounded to bf16 and INT8-quantised per row -> (codes, scales)."""
-    ldx = _mat(x, "x", (_bf16,))
-    M, K = x.shape
-    _arg(gamma, "gamma", _bf16, (K,))
-    _arg(beta, "beta", _bf16, (K,))
-    _on_current(x, gamma, beta)
-    q, s, ldq = _codes_out(out, x, M, K, stream)
-    _check(load().vit_ln_quant_int8(_p(x), M, K, ldx, _p(gamma), _p(beta), eps, _p(q), ldq, _p(s), _stream(stream)),
-           "vit_ln_quant_int8")
+    dev = _device(x, "x")
+    m, k, ldx = _mat(x, "x", dev, _BF16_ONLY)
+    g, b = _vec(gamma, "gamma", dev, _bf16, k), _vec(beta, "beta", dev, _bf16, k)
+    q, s, ldq = _codes_out(out, x, dev, m, k, stream)
+    _check(load().vit_ln_quant_int8(x.data_ptr(), m, k, ldx, g, b, eps, q.data_ptr(), ldq, s.data_ptr(),
+                                    _raw(stream, dev)), "vit_ln_quant_int8")
     return q, s
 
 
 def gelu_quant_int8(f, out=None, stream=None):
     """GELU(tanh) of bf16 f [M, K] (rows dense), rounded to bf16 and INT8-quantised per row -> (codes, scales)."""
-    ldf = _mat(f, "f", (_bf16,))
-    M, K = f.shape
-    _on_current(f)
-    q, s, ldq = _codes_out(out, f, M, K, stream)
-    _check(load().vit_gelu_quant_int8(_p(f), M, K, ldf, _p(q), ldq, _p(s), _stream(stream)), "vit_gelu_quant_int8")
+    dev = _device(f, "f")
+    m, k, ldf = _mat(f, "f", dev, _BF16_ONLY)
+    q, s, ldq = _codes_out(out, f, dev, m, k, stream)
+    _check(load().vit_gelu_quant_int8(f.data_ptr(), m, k, ldf, q.data_ptr(), ldq, s.data_ptr(), _raw(stream, dev)),
+           "vit_gelu_quant_int8")
     return q, s
 
 
 def int8_gemm(qa, sa, qw, sw, bias=None, residual=None, out=None, out_dtype=torch.bfloat16, stream=None):
     """C [M, N] = sa[m] sw[n] (qa . qw^T) (+ bias) (+ residual) from int8 codes qa [M, K], qw [N, K] (row strides
     of a multiple of 16) and fp32 scales sa [M], sw [N]; C, bias and residual bf16, fp16 or fp32 alike."""
-    lda = _mat(qa, "qa", (torch.int8,))
-    M, K = qa.shape
-    ldw = _mat(qw, "qw", (torch.int8,), K)
-    N = qw.shape[0]
-    _arg(sa, "sa", _f32, (M,))
-    _arg(sw, "sw", _f32, (N,))
+    dev = _device(qa, "qa")
+    m, k, lda = _mat(qa, "qa", dev, _I8_ONLY)
+    n, _, ldw = _mat(qw, "qw", dev, _I8_ONLY, None, k)
+    sa_p, sw_p = _vec(sa, "sa", dev, _f32, m), _vec(sw, "sw", dev, _f32, n)
+    ldc = n
     if out is not None:
         out_dtype = out.dtype
     if out_dtype not in _DTYPES:
         raise VitqError(f"out_dtype: {out_dtype}, expected bf16, fp16 or fp32")
-    t = (out_dtype,)
-    ldr = 0
+    if out is not None:
+        ldc = _mat(out, "out", dev, _DTYPES, m, n)[2]
+    bias_p, res_p, ldr = None, None, 0
     if bias is not None:
-        _arg(bias, "bias", out_dtype, (N,))
+        bias_p = _vec(bias, "bias", dev, out_dtype, n)
     if residual is not None:
-        ldr = _mat(residual, "residual", t, N, M)
-    _on_current(qa, sa, qw, sw, bias, residual, out)
+        ldr = _mat(residual, "residual", dev, (out_dtype,), m, n)[2]
+        res_p = residual.data_ptr()
     if out is None:
-        out = _new((M, N), out_dtype, qa, stream)
-        ldc = N
-    else:
-        ldc = _mat(out, "out", t, N, M)
-    _check(load().int8_gemm(_p(qa), lda, _p(sa), _p(qw), ldw, _p(sw), _p(bias), _p(residual), ldr, _p(out), ldc,
-                            _DTYPES[out_dtype], M, N, K, _stream(stream)), "int8_gemm")
+        out = _new(qa, (m, n), out_dtype, stream)
+    _check(load().int8_gemm(qa.data_ptr(), lda, sa_p, qw.data_ptr(), ldw, sw_p, bias_p, res_p, ldr, out.data_ptr(),
+                            ldc, _DTYPES[out_dtype], m, n, k, _raw(stream, dev)), "int8_gemm")
     return out
 
 
 ROPE_INTERLEAVED, ROPE_AXIS_FREQ, ROPE_ADJACENT, ROPE_INVERSE = 1, 2, 4, 8
+_ROPE_PACK = struct.Struct("=10id10q").pack   # the fields of RopeAxes, which has no padding
 
 
-def _heads(t, name, n=None, dtype=None, like=None):
-    """Check a [tokens, heads, head_dim] tensor with a dense innermost dimension."""
-    if not isinstance(t, torch.Tensor):
-        raise VitqError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
-    if t.device.type != _DEVICE_TYPE:
-        raise VitqError(f"{name}: tensor on {t.device}; the library reads device memory only")
-    if t.dtype not in _DTYPES or (dtype is not None and t.dtype != dtype):
-        raise VitqError(f"{name}: dtype {t.dtype}, expected {dtype or 'bf16, fp16 or fp32'}")
-    if t.dim() != 3 or (n is not None and t.shape[0] != n) or (like is not None and t.shape != like.shape):
-        raise VitqError(f"{name}: shape {tuple(t.shape)}, expected {tuple(like.shape) if like is not None else 'three dims'}")
-    if t.shape[2] > 1 and t.stride(2) != 1:
-        raise VitqError(f"{name}: strides {t.stride()}, the innermost dimension must be dense")
+def _heads(t, name, dev, dtypes, n=None, h=None, d=None):
+    """Check a [tokens, heads, head_dim] tensor with a dense innermost dimension -> its shape and two strides."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype not in dtypes or t.dim() != 3:
+        raise _why(t, name, dev, dtypes, (n, h, d), "")
+    tn, th, td = t.shape
+    st, sh, sd = t.stride()
+    if (n is not None and tn != n) or (h is not None and th != h) or (d is not None and td != d) or (sd != 1 and td > 1):
+        raise _why(t, name, dev, dtypes, (n, h, d), "a dense innermost dimension")
+    return tn, th, td, st, sh
 
 
 def rope_axes(q, k, pos, sections, theta: float = 10000.0, interleaved: bool = False, axis_freq: bool = False,
@@ -501,34 +524,35 @@ def rope_axes(q, k, pos, sections, theta: float = 10000.0, interleaved: bool = F
     """Rotary over several position axes of q [n, hq, d] and k [n, hk, d] (k may be None; any strides, the innermost
     dense) with int32 positions pos [n, axes] and `sections` rotary pairs per axis -> (q', k'), new tensors or `out`.
     inverse=True turns back: the gradient of the rotary.  See vit_rope_axes for the flags."""
-    _heads(q, "q")
-    n, hq, d = q.shape
-    hk = 0
-    if k is not None:
-        _heads(k, "k", n, q.dtype)
-        hk = k.shape[1]
-        if k.shape[2] != d:
-            raise VitqError(f"k: head dim {k.shape[2]}, q has {d}")
+    dev = _device(q, "q")
+    n, hq, d, qt, qh = _heads(q, "q", dev, _DTYPES)
+    t = q.dtype
     axes = len(sections)
     if not 1 <= axes <= 4:
         raise VitqError(f"sections: {axes} axes, expected 1 to 4")
-    if pos.device.type != _DEVICE_TYPE or pos.dtype != _i32 or tuple(pos.shape) != (n, axes):
-        raise VitqError(f"pos: {pos.dtype} {tuple(pos.shape)} on {pos.device}, expected int32 {(n, axes)} on the device")
-    _on_current(q, k, pos)
+    if not isinstance(pos, torch.Tensor) or pos.get_device() != dev or pos.dtype is not _i32 or pos.shape != (n, axes):
+        raise _why(pos, "pos", dev, (_i32,), (n, axes), "")
+    hk = kt = kh = kot = koh = 0
+    k_p = ko_p = ko = None
+    if k is not None:
+        _, hk, _, kt, kh = _heads(k, "k", dev, (t,), n, None, d)
+        k_p = k.data_ptr()
     if out is None:
-        qo = _new((n, hq, d), q.dtype, q, stream)
-        ko = None if k is None else _new((n, hk, d), q.dtype, q, stream)
+        qo, qot, qoh = _new(q, (n, hq, d), t, stream), hq * d, d
+        if k is not None:
+            ko, kot, koh = _new(q, (n, hk, d), t, stream), hk * d, d
     else:
         qo, ko = out
-        _heads(qo, "out q", n, q.dtype, q)
+        qot, qoh = _heads(qo, "out q", dev, (t,), n, hq, d)[3:]
         if k is not None:
-            _heads(ko, "out k", n, q.dtype, k)
-        _on_current(qo, ko)
+            kot, koh = _heads(ko, "out k", dev, (t,), n, hk, d)[3:]
+    if k is not None:
+        ko_p = ko.data_ptr()
     flags = (ROPE_INTERLEAVED * interleaved | ROPE_AXIS_FREQ * axis_freq | ROPE_ADJACENT * adjacent |
              ROPE_INVERSE * inverse)
-    p = RopeAxes(_DTYPES[q.dtype], axes, (C.c_int32 * 4)(*sections), hq, hk, d, flags, theta, *q.stride()[:2],
-                 *qo.stride()[:2], *(k.stride()[:2] + ko.stride()[:2] if hk else (0, 0, 0, 0)), *pos.stride())
-    _check(load().vit_rope_axes(C.byref(p), _p(q), _p(qo), _p(k), _p(ko), _p(pos), n, _stream(stream)),
+    p = _ROPE_PACK(_DTYPES[t], axes, *sections, *(0,) * (4 - axes), hq, hk, d, flags, theta, qt, qh, qot, qoh,
+                   kt, kh, kot, koh, *pos.stride())
+    _check(load().vit_rope_axes(p, q.data_ptr(), qo.data_ptr(), k_p, ko_p, pos.data_ptr(), n, _raw(stream, dev)),
            "vit_rope_axes")
     return qo, ko
 

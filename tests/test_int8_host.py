@@ -194,12 +194,12 @@ def test_binding_marshals_rope(on_cpu):
     pos = torch.zeros((3, 10), dtype=torch.int32).t()
     yq, yk = vitq.rope_axes(q, k, pos, (12, 12, 12), axis_freq=True, inverse=True)
     name, a = on_cpu.calls[-1]
-    p = a[0]._obj
+    p = vitq.RopeAxes.from_buffer_copy(a[0])
     assert name == "vit_rope_axes" and a[6] == 10 and yq.is_contiguous() and yk.shape == (10, 16, 72)
     assert (p.q_token, p.q_head, p.q_out_token, p.q_out_head) == (3456, 72, 1152, 72)
     assert (p.pos_token, p.pos_axis, p.flags, p.head_dim) == (1, 10, 2 | 8, 72)
     assert vitq.rope_axes_(q, None, pos, (36, 0, 0))[0] is q
-    p = on_cpu.calls[-1][1][0]._obj
+    p = vitq.RopeAxes.from_buffer_copy(on_cpu.calls[-1][1][0])
     assert p.heads_k == 0 and p.q_out_token == 3456 and list(p.sections) == [36, 0, 0, 0]
 
 
