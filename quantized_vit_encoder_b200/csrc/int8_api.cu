@@ -39,11 +39,12 @@ int vit_ln_quant_int8(const void* x, int M, int K, int ldx, const void* gamma, c
   int r = rows_int8_check(x, M, K, ldx, q, ldq, s, 2);
   if (r) return r;
   VITQ_CHECK(al(gamma, 2) && al(beta, 2), VITQ_ERR_ALIGN);
-  r = current_device_ok(nullptr);
+  int sms = 0;
+  r = current_device_ok(&sms);
   if (r) return r;
   if (M == 0) return VITQ_OK;
   const RowsInt8 a{x, ldx, M, K, (const __nv_bfloat16*)gamma, (const __nv_bfloat16*)beta, (double)eps, q, ldq, s};
-  VITQ_LAUNCH("ln_quant_int8", S(stream), 0, 3.0 * M * K + 4.0 * M + 4.0 * K, launch_ln_quant_int8(a, S(stream)));
+  VITQ_LAUNCH("ln_quant_int8", S(stream), 0, 3.0 * M * K + 4.0 * M + 4.0 * K, launch_ln_quant_int8(a, sms, S(stream)));
   return VITQ_OK;
 }
 

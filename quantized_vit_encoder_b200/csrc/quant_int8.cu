@@ -141,10 +141,20 @@ template <class T>
 __device__ __forceinline__ void store_codes(const uint4& u, const RowScale& c, int8_t* qr, int col, int K) {
   constexpr int PER = Elem<T>::PER;
   uint32_t w[PER / 4];
+  if (Elem<T>::kMove && c.mode == 0) {   // two values a multiply and an add
+    const uint64_t r = f2pack(c.r, c.r), magic = f2pack(12582912.0f, 12582912.0f);
+#pragma unroll
+    for (int g = 0; g < PER / 4; ++g) {
+      const float2 a = f2unpack(fadd2(fmul2(f2pack(Elem<T>::at(u, 4 * g), Elem<T>::at(u, 4 * g + 1)), r), magic));
+      const float2 b = f2unpack(fadd2(fmul2(f2pack(Elem<T>::at(u, 4 * g + 2), Elem<T>::at(u, 4 * g + 3)), r), magic));
+      w[g] = pack4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
+    }
+  } else {
 #pragma unroll
   for (int g = 0; g < PER / 4; ++g)
     w[g] = pack4(code_of<T>(Elem<T>::at(u, 4 * g), c), code_of<T>(Elem<T>::at(u, 4 * g + 1), c),
                  code_of<T>(Elem<T>::at(u, 4 * g + 2), c), code_of<T>(Elem<T>::at(u, 4 * g + 3), c));
+  }
   if (col + PER <= K) {
     if (PER == 8) *reinterpret_cast<uint2*>(qr + col) = make_uint2(w[0], w[PER / 4 - 1]);
     else *reinterpret_cast<uint32_t*>(qr + col) = w[0];
@@ -219,11 +229,9 @@ __device__ __forceinline__ uint32_t gelu_bits(uint32_t x) { return g_gelu_table[
 // read once.  Rows 16-byte aligned.
 template <int OP, class T, int TPR, int NC>
 __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR)
-    rows_int8_kernel(const T* __restrict__ x, int ldx, int M, int K, const __nv_bfloat16* __restrict__ gamma,
-                     const __nv_bfloat16* __restrict__ beta, double eps, int8_t* __restrict__ q, int ldq,
+    rows_int8_kernel(const T* __restrict__ x, int ldx, int M, int K, int8_t* __restrict__ q, int ldq,
                      float* __restrict__ s) {
   constexpr int PER = Elem<T>::PER;
-  __shared__ double sh_sum[32];
   __shared__ uint32_t sh_max[32];
   pdl_trigger();
   pdl_wait();
@@ -236,39 +244,6 @@ __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR)
   for (int c = 0; c < NC; ++c) {
     const int col = (c * TPR + t) * PER;
     u[c] = col < K ? load_chunk16(xr, col, K) : make_uint4(0u, 0u, 0u, 0u);
-  }
-  if (OP == kI8Ln) {
-    double s1 = 0.0;
-#pragma unroll
-    for (int c = 0; c < NC; ++c)
-#pragma unroll
-      for (int i = 0; i < PER; ++i) s1 += (double)Elem<T>::at(u[c], i);
-    const double mean = row_sum<TPR>(s1, sh_sum) / (double)K;
-    double s2 = 0.0;
-#pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      const int col = (c * TPR + t) * PER;
-#pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const double d = (double)Elem<T>::at(u[c], i) - mean;
-        if (col + i < K) s2 = fma(d, d, s2);
-      }
-    }
-    const double rstd = 1.0 / sqrt(row_sum<TPR>(s2, sh_sum) / (double)K + eps);
-#pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      const int col = (c * TPR + t) * PER;
-      if (col < K) {
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-          uint32_t h = 0u;
-          if (col + i < K)
-            h = ln_fp64(Elem<T>::at(u[c], i), __bfloat162float(gamma[col + i]), __bfloat162float(beta[col + i]), mean, rstd);
-          uint32_t& w = (&u[c].x)[i >> 1];
-          w = (i & 1) ? (w & 0xFFFFu) | (h << 16) : (w & 0xFFFF0000u) | h;
-        }
-      }
-    }
   }
   if (OP == kI8Gelu) {
 #pragma unroll
@@ -286,6 +261,172 @@ __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR)
     if (col < K) store_codes<T>(u[c], sc, q + (size_t)row * ldq, col, K);
   }
   if (t == 0) s[row] = sc.s;
+}
+
+// ---------------------------------------------------------------- LayerNorm
+// TPR threads per row (a warp, or a CTA of 128), the row in registers (at most NC
+// chunks of 8 columns a thread) and the next row's loads in flight; gamma and beta
+// staged once per CTA as fp32.  Persistent over the rows.
+//
+// Statistics: exact fp64 sums of x and x^2 (bf16 -> fp64 is exact); where the mean is
+// far above the spread (E[x^2] > 64 var), which would cost the difference its bits,
+// the squares are summed again around the mean.
+// y = (x - mean) rstd gamma + beta in fp32, mean as a sum of two fp32 numbers: x - mh,
+// (x - mh) r - ml r, and the last FMA round once each and r = fl32(rstd) once, so
+// |error| <= 3 2^-24 (|y| + |beta|) + 2^-24 |y| < (|y| + |beta|) 2^-21.  Where y minus and
+// plus that bound round to the same bf16 value, that value is the rounding of the exact
+// y; the other pairs (about 1 in 2^12) are evaluated in fp64.  Rows whose statistics are
+// not finite, or whose rstd leaves 2^-100 .. 2^100, are evaluated in fp64 as a whole.
+__device__ __noinline__ uint32_t ln_pair_exact(float x0, float x1, float g0, float g1, float b0, float b1, double mean,
+                                               double rstd) {
+  return bf16_bits_fp64(((double)x0 - mean) * rstd * (double)g0 + (double)b0) |
+         (bf16_bits_fp64(((double)x1 - mean) * rstd * (double)g1 + (double)b1) << 16);
+}
+
+// Makes the compiler unpack the chunks again where they are used next, instead of
+// keeping their 8 NC values in registers.
+template <int NC>
+__device__ __forceinline__ void unpack_again(uint4 (&u)[NC]) {
+#pragma unroll
+  for (int c = 0; c < NC; ++c) asm volatile("" : "+r"(u[c].x), "+r"(u[c].y), "+r"(u[c].z), "+r"(u[c].w));
+}
+
+template <int TPR, int NC>
+__global__ void __launch_bounds__(128, NC == 5 ? 5 : 3)
+    ln_rows_int8_kernel(const __nv_bfloat16* __restrict__ x, int ldx, int M, int K,
+                        const __nv_bfloat16* __restrict__ gamma, const __nv_bfloat16* __restrict__ beta, double eps,
+                        int8_t* __restrict__ q, int ldq, float* __restrict__ s) {
+  using E = Elem<__nv_bfloat16>;
+  constexpr int ROWS = 128 / TPR;          // rows a CTA works on at a time
+  extern __shared__ float4 ln8_smem[];     // gamma, then beta: chunk c of thread t at (2c + half) * TPR + t
+  __shared__ double sh_sum[2][4];
+  __shared__ uint32_t sh_max[4];
+  const int t = threadIdx.x % TPR, warp = threadIdx.x >> 5;
+  float4* sg = ln8_smem;
+  float4* sb = ln8_smem + 2 * NC * TPR;
+  pdl_trigger();
+  pdl_wait();
+  int row = blockIdx.x * ROWS + threadIdx.x / TPR;
+  const int stride = gridDim.x * ROWS;
+  auto load_row = [&](int r, uint4 (&u)[NC]) {
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int col = (c * TPR + t) * 8;
+      u[c] = r < M && col < K ? load_chunk16(x + (size_t)r * ldx, col, K) : make_uint4(0u, 0u, 0u, 0u);
+    }
+  };
+  uint4 nxt[NC];
+  load_row(row, nxt);
+  for (int i = threadIdx.x; i < NC * TPR * 2; i += 128) {   // float4 of 4 columns
+    const int half = i / TPR & 1, c = i / (2 * TPR), col = (c * TPR + i % TPR) * 8 + half * 4;
+    float g[4], b[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      g[k] = col + k < K ? __bfloat162float(gamma[col + k]) : 0.f;
+      b[k] = col + k < K ? __bfloat162float(beta[col + k]) : 0.f;
+    }
+    sg[i] = make_float4(g[0], g[1], g[2], g[3]);
+    sb[i] = make_float4(b[0], b[1], b[2], b[3]);
+  }
+  __syncthreads();
+  const double rK = 1.0 / (double)K;
+  for (; row < M; row += stride) {   // uniform over the threads of a row
+    uint4 u[NC];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) u[c] = nxt[c];
+    load_row(row + stride, nxt);
+    auto sum2 = [&](double& a, double& b) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        a += __shfl_xor_sync(0xffffffffu, a, o);
+        b += __shfl_xor_sync(0xffffffffu, b, o);
+      }
+      if (TPR > 32) {
+        __syncthreads();
+        if ((threadIdx.x & 31) == 0) {
+          sh_sum[0][warp] = a;
+          sh_sum[1][warp] = b;
+        }
+        __syncthreads();
+        a = (sh_sum[0][0] + sh_sum[0][1]) + (sh_sum[0][2] + sh_sum[0][3]);
+        b = (sh_sum[1][0] + sh_sum[1][1]) + (sh_sum[1][2] + sh_sum[1][3]);
+      }
+    };
+    double s1 = 0.0, s2 = 0.0, t1 = 0.0, t2 = 0.0;
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) {
+        const double a = (double)E::at(u[c], i), b = (double)E::at(u[c], i + 1);
+        s1 += a;
+        t1 += b;
+        s2 = fma(a, a, s2);
+        t2 = fma(b, b, t2);
+      }
+    s1 += t1;
+    s2 += t2;
+    sum2(s1, s2);
+    unpack_again(u);
+    const double mean = s1 * rK;
+    double var = fma(-mean, mean, s2 * rK);
+    if (!(s2 * rK <= 64.0 * var)) {   // also for a NaN
+      double d2 = 0.0, none = 0.0;   // reads the row again: rare, and it keeps no registers for it
+#pragma unroll 1
+      for (int k = t; k < K; k += TPR) {
+        const double d = (double)__bfloat162float(x[(size_t)row * ldx + k]) - mean;
+        d2 = fma(d, d, d2);
+      }
+      sum2(d2, none);
+      var = d2 * rK;
+    }
+    const double rstd = rsqrt(var + eps);
+    const float mh = (float)mean, ml = (float)(mean - (double)mh), r32 = (float)rstd;
+    const bool plain = r32 >= 0x1p-100f && r32 <= 0x1p100f && fabsf(mh) <= 0x1p100f;
+    const uint64_t nmh = f2pack(-mh, -mh), rr = f2pack(r32, r32), nmr = f2pack(-ml * r32, -ml * r32);
+    const uint64_t up = f2pack(0x1p-21f, 0x1p-21f), dn = f2pack(-0x1p-21f, -0x1p-21f);
+    uint32_t m = 0u;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int at = 2 * c * TPR + t;
+      const float4 g0 = sg[at], g1 = sg[at + TPR], b0 = sb[at], b1 = sb[at + TPR];
+      const float g[8] = {g0.x, g0.y, g0.z, g0.w, g1.x, g1.y, g1.z, g1.w};
+      const float b[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
+      uint32_t slow = 0u, h[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint64_t xc = fadd2(f2pack(E::at(u[c], 2 * i), E::at(u[c], 2 * i + 1)), nmh);
+        const uint64_t y = ffma2(ffma2(xc, rr, nmr), f2pack(g[2 * i], g[2 * i + 1]), f2pack(b[2 * i], b[2 * i + 1]));
+        const float2 yf = f2unpack(y);
+        const uint64_t e = f2pack(fabsf(yf.x) + fabsf(b[2 * i]), fabsf(yf.y) + fabsf(b[2 * i + 1]));
+        h[i] = bf16x2_of(ffma2(e, dn, y));
+        slow |= (uint32_t)(h[i] != bf16x2_of(ffma2(e, up, y))) << i;
+      }
+      if (!plain) slow = 15u;
+      if (slow) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if ((slow >> i) & 1u)
+            h[i] = ln_pair_exact(E::at(u[c], 2 * i), E::at(u[c], 2 * i + 1), g[2 * i], g[2 * i + 1], b[2 * i],
+                                 b[2 * i + 1], mean, rstd);
+      }
+      u[c] = make_uint4(h[0], h[1], h[2], h[3]);
+      // columns past K have gamma = beta = 0, so y = 0 (or NaN, in a row that has one anyway)
+      m = max(m, chunk_mag<__nv_bfloat16>(u[c]));
+    }
+    m = __reduce_max_sync(0xffffffffu, m);
+    if (TPR > 32) {
+      if ((threadIdx.x & 31) == 0) sh_max[warp] = m;
+      __syncthreads();
+      m = max(max(sh_max[0], sh_max[1]), max(sh_max[2], sh_max[3]));
+    }
+    const RowScale sc = row_scale<__nv_bfloat16>(m);
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int col = (c * TPR + t) * 8;
+      if (col < K) store_codes<__nv_bfloat16>(u[c], sc, q + (size_t)row * ldq, col, K);
+    }
+    if (t == 0) s[row] = sc.s;
+  }
 }
 
 // ---------------------------------------------------------------- any layout
@@ -344,14 +485,39 @@ template <int OP, class T, int TPR, int NC>
 cudaError_t rows_launch(const RowsInt8& a, cudaStream_t st) {
   const unsigned grid = TPR == 32 ? (unsigned)((a.M + 7) / 8) : (unsigned)a.M;
   return launch_pdl(rows_int8_kernel<OP, T, TPR, NC>, dim3(grid), dim3(TPR == 32 ? 256 : TPR), 0, st, (const T*)a.x,
-                    a.ldx, a.M, a.K, a.gamma, a.beta, a.eps, a.q, a.ldq, a.s);
+                    a.ldx, a.M, a.K, a.q, a.ldq, a.s);
+}
+
+template <class T>
+bool rows_aligned(const RowsInt8& a) {
+  return (reinterpret_cast<uintptr_t>(a.x) & 15u) == 0 && ((size_t)a.ldx * sizeof(T)) % 16 == 0;
+}
+
+template <int OP, class T>
+cudaError_t rows_any_launch(const RowsInt8& a, cudaStream_t st) {
+  return launch_pdl(rows_int8_any_kernel<OP, T>, dim3((unsigned)a.M), dim3(kAnyThreads), 0, st, (const T*)a.x, a.ldx,
+                    a.M, a.K, a.gamma, a.beta, a.eps, a.q, a.ldq, a.s);
+}
+
+template <int TPR, int NC>
+cudaError_t ln_rows_launch(const RowsInt8& a, int num_sms, cudaStream_t st) {
+  constexpr int ROWS = 128 / TPR;
+  constexpr size_t smem = (size_t)4 * NC * TPR * sizeof(float4);
+  constexpr int per_sm = NC == 5 ? 5 : 3;   // CTAs that fit an SM
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(ln_rows_int8_kernel<TPR, NC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  const long long ctas = ((long long)a.M + ROWS - 1) / ROWS, most = (long long)num_sms * per_sm;
+  return launch_pdl(ln_rows_int8_kernel<TPR, NC>, dim3((unsigned)(ctas < most ? ctas : most)), dim3(128), smem, st,
+                    (const __nv_bfloat16*)a.x, a.ldx, a.M, a.K, a.gamma, a.beta, a.eps, a.q, a.ldq, a.s);
 }
 
 template <int OP, class T>
 cudaError_t rows_dispatch(const RowsInt8& a, cudaStream_t st) {
-  const bool aligned = (reinterpret_cast<uintptr_t>(a.x) & 15u) == 0 && ((size_t)a.ldx * sizeof(T)) % 16 == 0;
   const int chunks = (a.K + Elem<T>::PER - 1) / Elem<T>::PER;
-  if (aligned && chunks <= 8192) {
+  if (rows_aligned<T>(a) && chunks <= 8192) {
     if (chunks <= 160) return rows_launch<OP, T, 32, 5>(a, st);
     if (chunks <= 256) return rows_launch<OP, T, 32, 8>(a, st);
     if (chunks <= 640) return rows_launch<OP, T, 128, 5>(a, st);
@@ -359,8 +525,7 @@ cudaError_t rows_dispatch(const RowsInt8& a, cudaStream_t st) {
     if (chunks <= 2048) return rows_launch<OP, T, 256, 8>(a, st);
     return rows_launch<OP, T, 1024, 8>(a, st);
   }
-  return launch_pdl(rows_int8_any_kernel<OP, T>, dim3((unsigned)a.M), dim3(kAnyThreads), 0, st, (const T*)a.x, a.ldx,
-                    a.M, a.K, a.gamma, a.beta, a.eps, a.q, a.ldq, a.s);
+  return rows_any_launch<OP, T>(a, st);
 }
 
 }  // namespace
@@ -371,8 +536,16 @@ cudaError_t launch_quant_int8(const RowsInt8& a, int dtype, cudaStream_t st) {
   if (dtype == 1) return rows_dispatch<kI8Plain, __half>(a, st);
   return rows_dispatch<kI8Plain, float>(a, st);
 }
-cudaError_t launch_ln_quant_int8(const RowsInt8& a, cudaStream_t st) {
-  return a.M == 0 ? cudaSuccess : rows_dispatch<kI8Ln, __nv_bfloat16>(a, st);
+cudaError_t launch_ln_quant_int8(const RowsInt8& a, int num_sms, cudaStream_t st) {
+  if (a.M == 0) return cudaSuccess;
+  const int chunks = (a.K + 7) / 8;
+  if (rows_aligned<__nv_bfloat16>(a)) {
+    if (chunks <= 160) return ln_rows_launch<32, 5>(a, num_sms, st);
+    if (chunks <= 256) return ln_rows_launch<32, 8>(a, num_sms, st);
+    if (chunks <= 640) return ln_rows_launch<128, 5>(a, num_sms, st);
+    if (chunks <= 1024) return ln_rows_launch<128, 8>(a, num_sms, st);
+  }
+  return rows_any_launch<kI8Ln, __nv_bfloat16>(a, st);
 }
 cudaError_t launch_gelu_quant_int8(const RowsInt8& a, cudaStream_t st) {
   return a.M == 0 ? cudaSuccess : rows_dispatch<kI8Gelu, __nv_bfloat16>(a, st);
