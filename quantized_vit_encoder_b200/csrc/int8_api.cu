@@ -24,12 +24,13 @@ int vit_quant_int8(const void* x, int dtype, int M, int K, int ldx, int8_t* q, i
   VITQ_CHECK(dtype_ok(dtype), VITQ_ERR_INVALID_ARG);
   int r = rows_int8_check(x, M, K, ldx, q, ldq, s, elem_bytes(dtype));
   if (r) return r;
-  r = current_device_ok(nullptr);
+  int sms = 0;
+  r = current_device_ok(&sms);
   if (r) return r;
   if (M == 0) return VITQ_OK;
   const RowsInt8 a{x, ldx, M, K, nullptr, nullptr, 0.0, q, ldq, s};
   VITQ_LAUNCH("quant_int8", S(stream), 0, (double)M * K * (elem_bytes(dtype) + 1) + 4.0 * M,
-              launch_quant_int8(a, dtype, S(stream)));
+              launch_quant_int8(a, dtype, sms, S(stream)));
   return VITQ_OK;
 }
 
@@ -51,11 +52,12 @@ int vit_ln_quant_int8(const void* x, int M, int K, int ldx, const void* gamma, c
 int vit_gelu_quant_int8(const void* f, int M, int K, int ldf, int8_t* q, int ldq, float* s, void* stream) {
   int r = rows_int8_check(f, M, K, ldf, q, ldq, s, 2);
   if (r) return r;
-  r = current_device_ok(nullptr);
+  int sms = 0;
+  r = current_device_ok(&sms);
   if (r) return r;
   if (M == 0) return VITQ_OK;
   const RowsInt8 a{f, ldf, M, K, nullptr, nullptr, 0.0, q, ldq, s};
-  VITQ_LAUNCH("gelu_quant_int8", S(stream), 0, 3.0 * M * K + 4.0 * M, launch_gelu_quant_int8(a, S(stream)));
+  VITQ_LAUNCH("gelu_quant_int8", S(stream), 0, 3.0 * M * K + 4.0 * M, launch_gelu_quant_int8(a, sms, S(stream)));
   return VITQ_OK;
 }
 

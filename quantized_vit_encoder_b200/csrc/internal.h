@@ -107,9 +107,9 @@ struct RowsInt8 {
   int ldq;
   float* s;
 };
-cudaError_t launch_quant_int8(const RowsInt8& a, int dtype, cudaStream_t st);
+cudaError_t launch_quant_int8(const RowsInt8& a, int dtype, int num_sms, cudaStream_t st);
 cudaError_t launch_ln_quant_int8(const RowsInt8& a, int num_sms, cudaStream_t st);
-cudaError_t launch_gelu_quant_int8(const RowsInt8& a, cudaStream_t st);
+cudaError_t launch_gelu_quant_int8(const RowsInt8& a, int num_sms, cudaStream_t st);
 
 // INT8 GEMM (gemm_int8.cu); dtype as VITQ_BF16 / VITQ_FP16 / VITQ_FP32 (bias, residual and C).
 struct Int8Gemm {

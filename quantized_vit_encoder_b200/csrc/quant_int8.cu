@@ -65,7 +65,7 @@ __device__ __forceinline__ uint32_t chunk_mag(const uint4& u) {
 // ---------------------------------------------------------------- codes of a row
 // How the codes of a row come from its scale s.  With s >= 2^-107 the product
 // p = y * r, r = fl32(1 / s), is within 2^-23 (relative) of y / s.  For bf16 values p
-// rounds like y / s once r is moved by 2^-21 in the right direction: with the 8-bit
+// (not rounded itself: one FMA adds it to 1.5 2^23, whose spacing is 1) rounds like y / s once r is moved by 2^-21 in the right direction: with the 8-bit
 // significands Y of y and A of amax, amax / 127 against y / (k + 1/2) is a comparison
 // of 254 Y 2^i with (2k + 1) A 2^j, integers below 2^16 times one power of two.
 // Either they differ by 2^-16 of their size, which the move and the roundings cannot
@@ -123,7 +123,7 @@ template <class T>
 __device__ __forceinline__ uint32_t code_of(float y, const RowScale& c) {
   if (c.mode == 0) {
     const float p = __fmul_rn(y, c.r);
-    if (Elem<T>::kMove) return rint_bits(p) & 0xFFu;
+    if (Elem<T>::kMove) return __float_as_uint(__fmaf_rn(y, c.r, 12582912.0f)) & 0xFFu;
     const uint32_t b = rint_bits(p);
     const float k = __fsub_rn(__uint_as_float(b), 12582912.0f);
     if (fabsf(__fsub_rn(p, k)) > 0.5f - 0x1p-14f) return code_near_tie(y, c.s, p) & 0xFFu;
@@ -137,16 +137,17 @@ __device__ __forceinline__ uint32_t pack4(uint32_t a, uint32_t b, uint32_t c, ui
 }
 
 // Codes of one chunk at column col of a row with K columns.
-template <class T>
-__device__ __forceinline__ void store_codes(const uint4& u, const RowScale& c, int8_t* qr, int col, int K) {
+// (qc: where they go).  TAIL: the chunk may reach past K.
+template <class T, bool TAIL>
+__device__ __forceinline__ void store_codes(const uint4& u, const RowScale& c, int8_t* qc, int col, int K) {
   constexpr int PER = Elem<T>::PER;
   uint32_t w[PER / 4];
-  if (Elem<T>::kMove && c.mode == 0) {   // two values a multiply and an add
+  if (Elem<T>::kMove && c.mode == 0) {   // two values an FMA
     const uint64_t r = f2pack(c.r, c.r), magic = f2pack(12582912.0f, 12582912.0f);
 #pragma unroll
     for (int g = 0; g < PER / 4; ++g) {
-      const float2 a = f2unpack(fadd2(fmul2(f2pack(Elem<T>::at(u, 4 * g), Elem<T>::at(u, 4 * g + 1)), r), magic));
-      const float2 b = f2unpack(fadd2(fmul2(f2pack(Elem<T>::at(u, 4 * g + 2), Elem<T>::at(u, 4 * g + 3)), r), magic));
+      const float2 a = f2unpack(ffma2(f2pack(Elem<T>::at(u, 4 * g), Elem<T>::at(u, 4 * g + 1)), r, magic));
+      const float2 b = f2unpack(ffma2(f2pack(Elem<T>::at(u, 4 * g + 2), Elem<T>::at(u, 4 * g + 3)), r, magic));
       w[g] = pack4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
     }
   } else {
@@ -155,22 +156,35 @@ __device__ __forceinline__ void store_codes(const uint4& u, const RowScale& c, i
     w[g] = pack4(code_of<T>(Elem<T>::at(u, 4 * g), c), code_of<T>(Elem<T>::at(u, 4 * g + 1), c),
                  code_of<T>(Elem<T>::at(u, 4 * g + 2), c), code_of<T>(Elem<T>::at(u, 4 * g + 3), c));
   }
-  if (col + PER <= K) {
-    if (PER == 8) *reinterpret_cast<uint2*>(qr + col) = make_uint2(w[0], w[PER / 4 - 1]);
-    else *reinterpret_cast<uint32_t*>(qr + col) = w[0];
+  if (!TAIL || col + PER <= K) {
+    if (PER == 8) *reinterpret_cast<uint2*>(qc) = make_uint2(w[0], w[PER / 4 - 1]);
+    else *reinterpret_cast<uint32_t*>(qc) = w[0];
   } else {
 #pragma unroll
     for (int i = 0; i < PER; ++i)
-      if (col + i < K) qr[col + i] = (int8_t)(w[i >> 2] >> (8 * (i & 3)));
+      if (col + i < K) qc[i] = (int8_t)(w[i >> 2] >> (8 * (i & 3)));
   }
 }
 
 // ---------------------------------------------------------------- loads
+// The chunk at column col of a row of K columns (zeros past K) from a row of any
+// alignment: 16 bytes at once where the row allows it, else 4-byte words, shifted by half
+// a word in rows that start on one.  Nothing outside the row is read.
 template <class T>
-__device__ __forceinline__ uint4 load_chunk16(const T* xr, int col, int K) {
+__device__ __forceinline__ uint4 load_chunk_any(const T* xr, int col, int K) {
   constexpr int PER = Elem<T>::PER;
-  if (col + PER <= K) return *reinterpret_cast<const uint4*>(xr + col);
   uint4 u = make_uint4(0u, 0u, 0u, 0u);
+  if (col + PER <= K) {
+    const uint32_t* p = reinterpret_cast<const uint32_t*>(reinterpret_cast<uintptr_t>(xr + col) & ~uintptr_t(3));
+    const uint32_t off = (uint32_t)reinterpret_cast<uintptr_t>(xr + col) & 15u;
+    if (off == 0) return *reinterpret_cast<const uint4*>(p);
+    if (PER == 4 || (off & 2u) == 0) return make_uint4(p[0], p[1], p[2], p[3]);
+    const uint16_t* h = reinterpret_cast<const uint16_t*>(xr + col);
+    const uint32_t w0 = col > 0 ? p[0] : (uint32_t)h[0] << 16, w1 = p[1], w2 = p[2], w3 = p[3];
+    const uint32_t w4 = col + PER < K ? p[4] : (uint32_t)h[7];
+    return make_uint4(__byte_perm(w0, w1, 0x5432), __byte_perm(w1, w2, 0x5432), __byte_perm(w2, w3, 0x5432),
+                      __byte_perm(w3, w4, 0x5432));
+  }
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     if (col + i < K) {
@@ -224,157 +238,244 @@ __device__ __noinline__ uint32_t ln_fp64(float x, float g, float b, double mean,
 
 __device__ __forceinline__ uint32_t gelu_bits(uint32_t x) { return g_gelu_table[x & 0xFFFFu]; }
 
+// ---------------------------------------------------------------- GELU by table
+// The magnitudes 2^-14 .. 16 of the GELU table as shared-memory words: GELU(x) and
+// GELU(-x) in the low and high half of word bits(x) - kGeluLo (9 KB; lanes that differ
+// only in sign read one word).  Chunks with another value (zeros, infinities, about 1 in
+// 800 of a unit normal's) take the whole table from global memory.
+constexpr uint32_t kGeluLo = 0x3880u, kGeluN = 0x900u;
+
+__device__ __forceinline__ void gelu_stage(uint32_t* lut) {
+  for (int i = threadIdx.x; i < (int)kGeluN / 8; i += blockDim.x) {
+    const uint4 a = *reinterpret_cast<const uint4*>(g_gelu_table + kGeluLo + 8 * i);
+    const uint4 b = *reinterpret_cast<const uint4*>(g_gelu_table + 0x8000u + kGeluLo + 8 * i);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      lut[8 * i + 2 * k] = __byte_perm((&a.x)[k], (&b.x)[k], 0x5410);
+      lut[8 * i + 2 * k + 1] = __byte_perm((&a.x)[k], (&b.x)[k], 0x7632);
+    }
+  }
+}
+
+__device__ __noinline__ uint4 gelu_chunk_global(uint4 u) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) (&u.x)[j] = gelu_bits((&u.x)[j]) | (gelu_bits((&u.x)[j] >> 16) << 16);
+  return u;
+}
+
+__device__ __forceinline__ uint4 gelu_chunk(const uint4& u, const uint32_t* lut) {
+  const char* base = reinterpret_cast<const char*>(lut);
+  uint4 y;
+  uint32_t far = 0u;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t w = (&u.x)[j];
+    // (magnitude - kGeluLo) of both halves, wrapping around below kGeluLo
+    uint32_t t, ok;
+    asm("add.u16x2 %0, %1, %2;" : "=r"(t) : "r"(w & 0x7FFF7FFFu), "r"(0x00010001u * (0x10000u - kGeluLo)));
+    asm("min.u16x2 %0, %1, %2;" : "=r"(ok) : "r"(t), "r"(0x00010001u * (kGeluN - 1u)));
+    far |= t ^ ok;
+    const uint32_t at = ok * 4u + ((w >> 14) & 0x00020002u);   // byte offsets; each half stays below 2^16
+    const uint32_t lo = *reinterpret_cast<const uint16_t*>(base + (at & 0xFFFFu));
+    const uint32_t hi = *reinterpret_cast<const uint16_t*>(base + (at >> 16));
+    (&y.x)[j] = __byte_perm(lo, hi, 0x5410);
+  }
+  return far ? gelu_chunk_global(u) : y;
+}
+
 // ---------------------------------------------------------------- the row kernel
-// TPR threads per row, the row held in registers as at most NC chunks per thread,
-// read once.  Rows 16-byte aligned.
-template <int OP, class T, int TPR, int NC>
+// TPR threads per row, the row held in registers as at most NC chunks per thread, read
+// once.  ANY: rows of any alignment and K; otherwise whole 16-byte chunks.  Plain rows: one
+// CTA for each (or 8 rows, a warp each); GELU: persistent over the rows, since every CTA
+// stages the table.
+template <int OP, class T, int TPR, int NC, bool ANY>
 __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR)
     rows_int8_kernel(const T* __restrict__ x, int ldx, int M, int K, int8_t* __restrict__ q, int ldq,
                      float* __restrict__ s) {
   constexpr int PER = Elem<T>::PER;
+  constexpr int ROWS = TPR == 32 ? 8 : 1;
   __shared__ uint32_t sh_max[32];
+  __shared__ __align__(16) uint32_t lut[OP == kI8Gelu ? kGeluN : 1];
   pdl_trigger();
+  if (OP == kI8Gelu) {   // the table is this library's own, written before its first launch
+    gelu_stage(lut);
+    __syncthreads();
+  }
   pdl_wait();
-  const int row = TPR == 32 ? blockIdx.x * 8 + (threadIdx.x >> 5) : blockIdx.x;
   const int t = TPR == 32 ? threadIdx.x & 31 : threadIdx.x;
-  if (row >= M) return;   // whole warps (TPR = 32) or whole CTAs
-  const T* xr = x + (size_t)row * ldx;
-  uint4 u[NC];
+  for (int row = blockIdx.x * ROWS + (TPR == 32 ? threadIdx.x >> 5 : 0); row < M; row += gridDim.x * ROWS) {
+    const T* xt = x + (size_t)row * ldx + t * PER;   // whole warps (TPR = 32) or whole CTAs share a row
+    uint4 u[NC];
 #pragma unroll
-  for (int c = 0; c < NC; ++c) {
-    const int col = (c * TPR + t) * PER;
-    u[c] = col < K ? load_chunk16(xr, col, K) : make_uint4(0u, 0u, 0u, 0u);
+    for (int c = 0; c < NC; ++c) {
+      const int col = (c * TPR + t) * PER;
+      u[c] = make_uint4(0u, 0u, 0u, 0u);
+      if (col < K) u[c] = ANY ? load_chunk_any(xt - t * PER, col, K) : *reinterpret_cast<const uint4*>(xt + c * TPR * PER);
+    }
+    uint32_t m = 0u;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      if (OP == kI8Gelu && (c * TPR + t) * PER < K) u[c] = gelu_chunk(u[c], lut);
+      m = max(m, chunk_mag<T>(u[c]));
+    }
+    const RowScale sc = row_scale<T>(row_max<TPR>(m, sh_max));
+    int8_t* qt = q + (size_t)row * ldq + t * PER;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int col = (c * TPR + t) * PER;
+      if (col < K) store_codes<T, ANY>(u[c], sc, qt + c * TPR * PER, col, K);
+    }
+    if (t == 0) s[row] = sc.s;
   }
-  if (OP == kI8Gelu) {
-#pragma unroll
-    for (int c = 0; c < NC; ++c)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) (&u[c].x)[j] = gelu_bits((&u[c].x)[j]) | (gelu_bits((&u[c].x)[j] >> 16) << 16);
-  }
-  uint32_t m = 0u;
-#pragma unroll
-  for (int c = 0; c < NC; ++c) m = max(m, chunk_mag<T>(u[c]));
-  const RowScale sc = row_scale<T>(row_max<TPR>(m, sh_max));
-#pragma unroll
-  for (int c = 0; c < NC; ++c) {
-    const int col = (c * TPR + t) * PER;
-    if (col < K) store_codes<T>(u[c], sc, q + (size_t)row * ldq, col, K);
-  }
-  if (t == 0) s[row] = sc.s;
 }
 
 // ---------------------------------------------------------------- LayerNorm
-// TPR threads per row (a warp, or a CTA of 128), the row in registers (at most NC
-// chunks of 8 columns a thread) and the next row's loads in flight; gamma and beta
-// staged once per CTA as fp32.  Persistent over the rows.
+// TPR threads per row: half a warp, a warp, or a CTA of 128.  A thread's chunks (8 columns
+// each) go to shared memory by 16-byte asynchronous copies and stay there, private to the
+// thread, through the three passes over them (statistics, normalised bf16 values in place,
+// codes): the loops stay rolled and the registers few, so that 32 warps share an SM and
+// hide each other's latencies.  (Held in registers, 36 a thread, the same arithmetic ran
+// 20 warps an SM, missed the instruction cache and took 33.6 us against 25024 x 1152.)
+// gamma and beta are staged once per CTA as fp32; persistent over the rows.
 //
 // Statistics: exact fp64 sums of x and x^2 (bf16 -> fp64 is exact); where the mean is
-// far above the spread (E[x^2] > 64 var), which would cost the difference its bits,
+// far above the spread (E[x^2] > 2^10 var), which would cost the difference its bits,
 // the squares are summed again around the mean.
 // y = (x - mean) rstd gamma + beta in fp32, mean as a sum of two fp32 numbers: x - mh,
 // (x - mh) r - ml r, and the last FMA round once each and r = fl32(rstd) once, so
 // |error| <= 3 2^-24 (|y| + |beta|) + 2^-24 |y| < (|y| + |beta|) 2^-21.  Where y minus and
 // plus that bound round to the same bf16 value, that value is the rounding of the exact
-// y; the other pairs (about 1 in 2^12) are evaluated in fp64.  Rows whose statistics are
+// y; the other values (about 1 in 2^12) are evaluated in fp64.  Rows whose statistics are
 // not finite, or whose rstd leaves 2^-100 .. 2^100, are evaluated in fp64 as a whole.
-__device__ __noinline__ uint32_t ln_pair_exact(float x0, float x1, float g0, float g1, float b0, float b1, double mean,
-                                               double rstd) {
-  return bf16_bits_fp64(((double)x0 - mean) * rstd * (double)g0 + (double)b0) |
-         (bf16_bits_fp64(((double)x1 - mean) * rstd * (double)g1 + (double)b1) << 16);
-}
 
-// Makes the compiler unpack the chunks again where they are used next, instead of
-// keeping their 8 NC values in registers.
-template <int NC>
-__device__ __forceinline__ void unpack_again(uint4 (&u)[NC]) {
+// The bf16 results of one chunk (v: its 8 values; g, b: two float4 of gamma and of beta, the
+// second `step` behind the first): fp32 where the bracket decides, else (or where !plain) fp64.
+__device__ __noinline__ uint4 ln_chunk_exact(const uint4 v, const float4* g, const float4* b, int step, double mean,
+                                             double rstd, bool plain) {
+  using E = Elem<__nv_bfloat16>;
+  const float mh = (float)mean, ml = (float)(mean - (double)mh), r32 = (float)rstd;
+  uint4 out;
 #pragma unroll
-  for (int c = 0; c < NC; ++c) asm volatile("" : "+r"(u[c].x), "+r"(u[c].y), "+r"(u[c].z), "+r"(u[c].w));
+  for (int i = 0; i < 4; ++i) {
+    const float2 gv = reinterpret_cast<const float2*>(g + (i >> 1) * step)[i & 1];
+    const float2 bv = reinterpret_cast<const float2*>(b + (i >> 1) * step)[i & 1];
+    const float x0 = E::at(v, 2 * i), x1 = E::at(v, 2 * i + 1);
+    const float y0 = fmaf(fmaf(x0 - mh, r32, -ml * r32), gv.x, bv.x), y1 = fmaf(fmaf(x1 - mh, r32, -ml * r32), gv.y, bv.y);
+    const float e0 = fabsf(y0) + fabsf(bv.x), e1 = fabsf(y1) + fabsf(bv.y);
+    uint32_t h = pack_bf16x2(fmaf(e0, -0x1p-21f, y0), fmaf(e1, -0x1p-21f, y1));
+    if (!plain || h != pack_bf16x2(fmaf(e0, 0x1p-21f, y0), fmaf(e1, 0x1p-21f, y1)))
+      h = bf16_bits_fp64(((double)x0 - mean) * rstd * (double)gv.x + (double)bv.x) |
+          (bf16_bits_fp64(((double)x1 - mean) * rstd * (double)gv.y + (double)bv.y) << 16);
+    (&out.x)[i] = h;
+  }
+  return out;
 }
 
-template <int TPR, int NC>
-__global__ void __launch_bounds__(128, NC == 5 ? 5 : 3)
-    ln_rows_int8_kernel(const __nv_bfloat16* __restrict__ x, int ldx, int M, int K,
+constexpr int kLn8Threads = 256;
+
+// nc chunks a thread (nc * TPR * 8 >= K).  TPR = 128: 128 threads a CTA.
+// ANY: rows of any alignment and K, loaded synchronously.
+template <int TPR, bool ANY>
+__global__ void __launch_bounds__(TPR == 128 ? 128 : kLn8Threads, TPR == 128 ? 8 : 4)
+    ln_rows_int8_kernel(const __nv_bfloat16* __restrict__ x, int ldx, int M, int K, int nc,
                         const __nv_bfloat16* __restrict__ gamma, const __nv_bfloat16* __restrict__ beta, double eps,
                         int8_t* __restrict__ q, int ldq, float* __restrict__ s) {
   using E = Elem<__nv_bfloat16>;
-  constexpr int ROWS = 128 / TPR;          // rows a CTA works on at a time
-  extern __shared__ float4 ln8_smem[];     // gamma, then beta: chunk c of thread t at (2c + half) * TPR + t
+  constexpr int LANES = TPR < 32 ? TPR : 32;
+  extern __shared__ float4 ln8_smem[];     // gamma, beta: chunk c of thread t at (2c + half) * TPR + t; then the chunks
   __shared__ double sh_sum[2][4];
   __shared__ uint32_t sh_max[4];
-  const int t = threadIdx.x % TPR, warp = threadIdx.x >> 5;
+  const int t = threadIdx.x % TPR, warp = threadIdx.x >> 5, rows = blockDim.x / TPR;
   float4* sg = ln8_smem;
-  float4* sb = ln8_smem + 2 * NC * TPR;
+  float4* sb = ln8_smem + 2 * nc * TPR;
+  uint4* mine = reinterpret_cast<uint4*>(ln8_smem + 4 * nc * TPR) + threadIdx.x;   // chunk c at c * blockDim.x
+  const int pitch = blockDim.x;
   pdl_trigger();
   pdl_wait();
-  int row = blockIdx.x * ROWS + threadIdx.x / TPR;
-  const int stride = gridDim.x * ROWS;
-  auto load_row = [&](int r, uint4 (&u)[NC]) {
-#pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      const int col = (c * TPR + t) * 8;
-      u[c] = r < M && col < K ? load_chunk16(x + (size_t)r * ldx, col, K) : make_uint4(0u, 0u, 0u, 0u);
+  // rows in groups, so that the warps that share rows (or a CTA) stay together to the end
+  int row0 = blockIdx.x * rows + (TPR < 32 ? warp * (32 / TPR) : TPR == 32 ? warp : 0);
+  const int sub = TPR < 32 ? (threadIdx.x & 31) / TPR : 0;
+  const int stride = gridDim.x * rows;
+  const uint32_t mine_s = smem_u32(mine);
+  auto fetch = [&](int r0) {   // a spare half warp repeats its neighbour's row
+    const __nv_bfloat16* xt = x + (size_t)(r0 + sub < M ? r0 + sub : r0) * ldx + t * 8;
+    uint32_t dst = mine_s;
+#pragma unroll 3
+    for (int c = 0, col = t * 8; c < nc; ++c, col += 8 * TPR, dst += 16 * pitch) {
+      if (ANY) {
+        mine[c * pitch] = col < K ? load_chunk_any(xt - t * 8, col, K) : make_uint4(0u, 0u, 0u, 0u);
+      } else {
+        cp_async16(dst, col < K ? xt + c * (8 * TPR) : x, col < K ? 16u : 0u);
+      }
     }
+    cp_async_commit();
   };
-  uint4 nxt[NC];
-  load_row(row, nxt);
-  for (int i = threadIdx.x; i < NC * TPR * 2; i += 128) {   // float4 of 4 columns
-    const int half = i / TPR & 1, c = i / (2 * TPR), col = (c * TPR + i % TPR) * 8 + half * 4;
-    float g[4], b[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      g[k] = col + k < K ? __bfloat162float(gamma[col + k]) : 0.f;
-      b[k] = col + k < K ? __bfloat162float(beta[col + k]) : 0.f;
+  if (row0 < M) fetch(row0);
+  const bool wide = !ANY && ((reinterpret_cast<uintptr_t>(gamma) | reinterpret_cast<uintptr_t>(beta)) & 15u) == 0;
+  for (int i = threadIdx.x; i < nc * TPR; i += blockDim.x) {   // 8 columns
+    const int col = i * 8;
+    uint4 gu = make_uint4(0u, 0u, 0u, 0u), bu = gu;
+    if (col < K) {
+      gu = wide ? *reinterpret_cast<const uint4*>(gamma + col) : load_chunk_any(gamma, col, K);
+      bu = wide ? *reinterpret_cast<const uint4*>(beta + col) : load_chunk_any(beta, col, K);
     }
-    sg[i] = make_float4(g[0], g[1], g[2], g[3]);
-    sb[i] = make_float4(b[0], b[1], b[2], b[3]);
+    const int at = (2 * (i / TPR)) * TPR + i % TPR;
+    sg[at] = make_float4(E::at(gu, 0), E::at(gu, 1), E::at(gu, 2), E::at(gu, 3));
+    sg[at + TPR] = make_float4(E::at(gu, 4), E::at(gu, 5), E::at(gu, 6), E::at(gu, 7));
+    sb[at] = make_float4(E::at(bu, 0), E::at(bu, 1), E::at(bu, 2), E::at(bu, 3));
+    sb[at + TPR] = make_float4(E::at(bu, 4), E::at(bu, 5), E::at(bu, 6), E::at(bu, 7));
   }
   __syncthreads();
   const double rK = 1.0 / (double)K;
-  for (; row < M; row += stride) {   // uniform over the threads of a row
-    uint4 u[NC];
+  auto sum2 = [&](double& a, double& b) {   // over the threads of a row
 #pragma unroll
-    for (int c = 0; c < NC; ++c) u[c] = nxt[c];
-    load_row(row + stride, nxt);
-    auto sum2 = [&](double& a, double& b) {
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        a += __shfl_xor_sync(0xffffffffu, a, o);
-        b += __shfl_xor_sync(0xffffffffu, b, o);
+    for (int o = LANES / 2; o > 0; o >>= 1) {
+      a += __shfl_xor_sync(0xffffffffu, a, o);
+      b += __shfl_xor_sync(0xffffffffu, b, o);
+    }
+    if (TPR > 32) {
+      __syncthreads();
+      if ((threadIdx.x & 31) == 0) {
+        sh_sum[0][warp] = a;
+        sh_sum[1][warp] = b;
       }
-      if (TPR > 32) {
-        __syncthreads();
-        if ((threadIdx.x & 31) == 0) {
-          sh_sum[0][warp] = a;
-          sh_sum[1][warp] = b;
-        }
-        __syncthreads();
-        a = (sh_sum[0][0] + sh_sum[0][1]) + (sh_sum[0][2] + sh_sum[0][3]);
-        b = (sh_sum[1][0] + sh_sum[1][1]) + (sh_sum[1][2] + sh_sum[1][3]);
-      }
-    };
+      __syncthreads();
+      a = (sh_sum[0][0] + sh_sum[0][1]) + (sh_sum[0][2] + sh_sum[0][3]);
+      b = (sh_sum[1][0] + sh_sum[1][1]) + (sh_sum[1][2] + sh_sum[1][3]);
+    }
+  };
+  for (; row0 < M; row0 += stride) {
+    const int row = row0 + sub;
+    cp_async_wait<0>();
     double s1 = 0.0, s2 = 0.0, t1 = 0.0, t2 = 0.0;
-#pragma unroll
-    for (int c = 0; c < NC; ++c)
+#pragma unroll 3
+    for (int c = 0; c < nc; ++c) {
+      const uint4 u = mine[c * pitch];
 #pragma unroll
       for (int i = 0; i < 8; i += 2) {
-        const double a = (double)E::at(u[c], i), b = (double)E::at(u[c], i + 1);
+        const double a = (double)E::at(u, i), b = (double)E::at(u, i + 1);
         s1 += a;
         t1 += b;
         s2 = fma(a, a, s2);
         t2 = fma(b, b, t2);
       }
+    }
     s1 += t1;
     s2 += t2;
     sum2(s1, s2);
-    unpack_again(u);
     const double mean = s1 * rK;
     double var = fma(-mean, mean, s2 * rK);
-    if (!(s2 * rK <= 64.0 * var)) {   // also for a NaN
-      double d2 = 0.0, none = 0.0;   // reads the row again: rare, and it keeps no registers for it
+    const bool again = !(s2 * rK <= 1024.0 * var);   // also for a NaN
+    if (TPR <= 32 ? __any_sync(0xffffffffu, again) : again) {   // the sums are the same in all threads of a row
+      double d2 = 0.0, none = 0.0;
 #pragma unroll 1
-      for (int k = t; k < K; k += TPR) {
-        const double d = (double)__bfloat162float(x[(size_t)row * ldx + k]) - mean;
-        d2 = fma(d, d, d2);
+      for (int c = 0; c < nc; ++c) {
+        const uint4 u = mine[c * pitch];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const double d = (double)E::at(u, i) - mean;
+          if ((c * TPR + t) * 8 + i < K) d2 = fma(d, d, d2);
+        }
       }
       sum2(d2, none);
       var = d2 * rK;
@@ -384,54 +485,63 @@ __global__ void __launch_bounds__(128, NC == 5 ? 5 : 3)
     const bool plain = r32 >= 0x1p-100f && r32 <= 0x1p100f && fabsf(mh) <= 0x1p100f;
     const uint64_t nmh = f2pack(-mh, -mh), rr = f2pack(r32, r32), nmr = f2pack(-ml * r32, -ml * r32);
     const uint64_t up = f2pack(0x1p-21f, 0x1p-21f), dn = f2pack(-0x1p-21f, -0x1p-21f);
-    uint32_t m = 0u;
-#pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      const int at = 2 * c * TPR + t;
-      const float4 g0 = sg[at], g1 = sg[at + TPR], b0 = sb[at], b1 = sb[at + TPR];
+    uint32_t m = 0u;   // bits of the largest |y|, whose bf16 rounding is the largest |bf16(y)|; a NaN is above all
+    const float4 *gp = sg + t, *bp = sb + t;
+    uint4* at = mine;
+#pragma unroll 1
+    for (int c = 0; c < nc; ++c, gp += 2 * TPR, bp += 2 * TPR, at += pitch) {
+      const uint4 u = *at;
+      const float4 g0 = gp[0], g1 = gp[TPR], b0 = bp[0], b1 = bp[TPR];
       const float g[8] = {g0.x, g0.y, g0.z, g0.w, g1.x, g1.y, g1.z, g1.w};
       const float b[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
-      uint32_t slow = 0u, h[4];
+      uint32_t h[4], differ = plain ? 0u : 1u;
+      float cm = 0.f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint64_t xc = fadd2(f2pack(E::at(u[c], 2 * i), E::at(u[c], 2 * i + 1)), nmh);
+        const uint64_t xc = fadd2(f2pack(E::at(u, 2 * i), E::at(u, 2 * i + 1)), nmh);
         const uint64_t y = ffma2(ffma2(xc, rr, nmr), f2pack(g[2 * i], g[2 * i + 1]), f2pack(b[2 * i], b[2 * i + 1]));
         const float2 yf = f2unpack(y);
         const uint64_t e = f2pack(fabsf(yf.x) + fabsf(b[2 * i]), fabsf(yf.y) + fabsf(b[2 * i + 1]));
         h[i] = bf16x2_of(ffma2(e, dn, y));
-        slow |= (uint32_t)(h[i] != bf16x2_of(ffma2(e, up, y))) << i;
+        differ |= h[i] ^ bf16x2_of(ffma2(e, up, y));
+        cm = fmax3(cm, fabsf(yf.x), fabsf(yf.y));
       }
-      if (!plain) slow = 15u;
-      if (slow) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if ((slow >> i) & 1u)
-            h[i] = ln_pair_exact(E::at(u[c], 2 * i), E::at(u[c], 2 * i + 1), g[2 * i], g[2 * i + 1], b[2 * i],
-                                 b[2 * i + 1], mean, rstd);
+      uint4 w = make_uint4(h[0], h[1], h[2], h[3]);
+      if (differ) {
+        w = ln_chunk_exact(u, gp, bp, TPR, mean, rstd, plain);
+        cm = E::of_mag(chunk_mag<__nv_bfloat16>(w));
       }
-      u[c] = make_uint4(h[0], h[1], h[2], h[3]);
       // columns past K have gamma = beta = 0, so y = 0 (or NaN, in a row that has one anyway)
-      m = max(m, chunk_mag<__nv_bfloat16>(u[c]));
+      m = max(m, __float_as_uint(cm));
+      *at = w;
     }
-    m = __reduce_max_sync(0xffffffffu, m);
+    if (TPR < 32) {
+#pragma unroll
+      for (int o = LANES / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    } else {
+      m = __reduce_max_sync(0xffffffffu, m);
+    }
     if (TPR > 32) {
       if ((threadIdx.x & 31) == 0) sh_max[warp] = m;
       __syncthreads();
       m = max(max(sh_max[0], sh_max[1]), max(sh_max[2], sh_max[3]));
     }
-    const RowScale sc = row_scale<__nv_bfloat16>(m);
-#pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      const int col = (c * TPR + t) * 8;
-      if (col < K) store_codes<__nv_bfloat16>(u[c], sc, q + (size_t)row * ldq, col, K);
+    const RowScale sc =
+        row_scale<__nv_bfloat16>((uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(m))) & 0x7FFFu);
+    if (row < M) {
+      int8_t* qt = q + (size_t)row * ldq + t * 8;
+#pragma unroll 3
+      for (int c = 0, col = t * 8; c < nc; ++c, col += 8 * TPR)
+        if (col < K) store_codes<__nv_bfloat16, ANY>(mine[c * pitch], sc, qt + c * (8 * TPR), col, K);
     }
-    if (t == 0) s[row] = sc.s;
+    if (row < M && t == 0) s[row] = sc.s;
+    if (row0 + stride < M) fetch(row0 + stride);
   }
 }
 
-// ---------------------------------------------------------------- any layout
-// Rows of any alignment and width: one CTA per row, single elements, the row read
-// again in each pass.
+// ---------------------------------------------------------------- any width
+// Rows too wide for the kernels above (K > 32768 in fp32; LayerNorm, K > 16384): one CTA
+// per row, single elements, the row read again in each pass.
 constexpr int kAnyThreads = 256;
 
 template <class T>
@@ -470,7 +580,7 @@ __global__ void __launch_bounds__(kAnyThreads)
     const uint32_t b = elem_bits(xr, k);
     if (OP == kI8Ln)
       return ln_fp64(value_of_bits<T>(b), __bfloat162float(gamma[k]), __bfloat162float(beta[k]), mean, rstd);
-    return OP == kI8Gelu ? gelu_bits(b) : b;
+    return b;
   };
   uint32_t m = 0u;
   for (int k = threadIdx.x; k < K; k += kAnyThreads) m = max(m, bits(k) & (sizeof(T) == 2 ? 0x7FFFu : 0x7FFFFFFFu));
@@ -481,16 +591,23 @@ __global__ void __launch_bounds__(kAnyThreads)
 }
 
 // ---------------------------------------------------------------- launch
-template <int OP, class T, int TPR, int NC>
-cudaError_t rows_launch(const RowsInt8& a, cudaStream_t st) {
-  const unsigned grid = TPR == 32 ? (unsigned)((a.M + 7) / 8) : (unsigned)a.M;
-  return launch_pdl(rows_int8_kernel<OP, T, TPR, NC>, dim3(grid), dim3(TPR == 32 ? 256 : TPR), 0, st, (const T*)a.x,
-                    a.ldx, a.M, a.K, a.q, a.ldq, a.s);
+// Rows that start on 16 bytes and hold whole chunks.
+template <class T>
+bool rows_whole(const RowsInt8& a) {
+  return (reinterpret_cast<uintptr_t>(a.x) & 15u) == 0 && ((size_t)a.ldx * sizeof(T)) % 16 == 0 &&
+         a.K % Elem<T>::PER == 0;
 }
 
-template <class T>
-bool rows_aligned(const RowsInt8& a) {
-  return (reinterpret_cast<uintptr_t>(a.x) & 15u) == 0 && ((size_t)a.ldx * sizeof(T)) % 16 == 0;
+template <int OP, class T, int TPR, int NC>
+cudaError_t rows_launch(const RowsInt8& a, int num_sms, cudaStream_t st) {
+  long long grid = TPR == 32 ? ((long long)a.M + 7) / 8 : a.M;
+  if (OP == kI8Gelu) {   // as many CTAs as fit the GPU (about 28 warps an SM)
+    const long long most = (long long)num_sms * (TPR == 32 ? 3 : TPR >= 1024 ? 1 : 896 / TPR);
+    if (grid > most) grid = most;
+  }
+  auto kern = rows_whole<T>(a) ? rows_int8_kernel<OP, T, TPR, NC, false> : rows_int8_kernel<OP, T, TPR, NC, true>;
+  return launch_pdl(kern, dim3((unsigned)grid), dim3(TPR == 32 ? 256 : TPR), 0, st, (const T*)a.x, a.ldx, a.M, a.K,
+                    a.q, a.ldq, a.s);
 }
 
 template <int OP, class T>
@@ -499,56 +616,56 @@ cudaError_t rows_any_launch(const RowsInt8& a, cudaStream_t st) {
                     a.M, a.K, a.gamma, a.beta, a.eps, a.q, a.ldq, a.s);
 }
 
-template <int TPR, int NC>
+template <int TPR>
 cudaError_t ln_rows_launch(const RowsInt8& a, int num_sms, cudaStream_t st) {
-  constexpr int ROWS = 128 / TPR;
-  constexpr size_t smem = (size_t)4 * NC * TPR * sizeof(float4);
-  constexpr int per_sm = NC == 5 ? 5 : 3;   // CTAs that fit an SM
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(ln_rows_int8_kernel<TPR, NC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)smem);
-    if (e != cudaSuccess) return e;
-  }
-  const long long ctas = ((long long)a.M + ROWS - 1) / ROWS, most = (long long)num_sms * per_sm;
-  return launch_pdl(ln_rows_int8_kernel<TPR, NC>, dim3((unsigned)(ctas < most ? ctas : most)), dim3(128), smem, st,
-                    (const __nv_bfloat16*)a.x, a.ldx, a.M, a.K, a.gamma, a.beta, a.eps, a.q, a.ldq, a.s);
+  const int nc = (a.K + 8 * TPR - 1) / (8 * TPR);
+  // as many threads a CTA as leave every SM one (gamma and beta are staged once a CTA)
+  int threads = TPR == 128 ? 128 : kLn8Threads;
+  while (threads > 32 && TPR < 128 && (long long)num_sms * threads / TPR > a.M) threads /= 2;
+  const size_t smem = (size_t)nc * 16 * (4 * TPR + threads);
+  auto kern = rows_whole<__nv_bfloat16>(a) ? ln_rows_int8_kernel<TPR, false> : ln_rows_int8_kernel<TPR, true>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  const int per_sm = (int)(220 * 1024 / (smem + 1024));
+  const int rows = threads / TPR;
+  const long long ctas = ((long long)a.M + rows - 1) / rows;
+  const long long most = (long long)num_sms * (per_sm < 1024 / threads ? per_sm : 1024 / threads);
+  return launch_pdl(kern, dim3((unsigned)(ctas < most ? ctas : most)), dim3(threads), smem, st,
+                    (const __nv_bfloat16*)a.x, a.ldx, a.M, a.K, nc, a.gamma, a.beta, a.eps, a.q, a.ldq, a.s);
 }
 
+// Threads a row: as few as hold it in 9 chunks each (5 for rows of up to 160).
 template <int OP, class T>
-cudaError_t rows_dispatch(const RowsInt8& a, cudaStream_t st) {
+cudaError_t rows_dispatch(const RowsInt8& a, int num_sms, cudaStream_t st) {
   const int chunks = (a.K + Elem<T>::PER - 1) / Elem<T>::PER;
-  if (rows_aligned<T>(a) && chunks <= 8192) {
-    if (chunks <= 160) return rows_launch<OP, T, 32, 5>(a, st);
-    if (chunks <= 256) return rows_launch<OP, T, 32, 8>(a, st);
-    if (chunks <= 640) return rows_launch<OP, T, 128, 5>(a, st);
-    if (chunks <= 1024) return rows_launch<OP, T, 128, 8>(a, st);
-    if (chunks <= 2048) return rows_launch<OP, T, 256, 8>(a, st);
-    return rows_launch<OP, T, 1024, 8>(a, st);
-  }
-  return rows_any_launch<OP, T>(a, st);
+  if (chunks <= 160) return rows_launch<OP, T, 32, 5>(a, num_sms, st);
+  if (chunks <= 288) return rows_launch<OP, T, 32, 9>(a, num_sms, st);
+  if (chunks <= 576) return rows_launch<OP, T, 64, 9>(a, num_sms, st);
+  if (chunks <= 1152) return rows_launch<OP, T, 128, 9>(a, num_sms, st);
+  if (chunks <= 2304) return rows_launch<OP, T, 256, 9>(a, num_sms, st);
+  if (sizeof(T) == 2 || chunks <= 8192) return rows_launch<OP, T, 1024, 8>(a, num_sms, st);   // 2 bytes: K <= 65536
+  if constexpr (sizeof(T) == 4) return rows_any_launch<OP, T>(a, st);
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace
 
-cudaError_t launch_quant_int8(const RowsInt8& a, int dtype, cudaStream_t st) {
+cudaError_t launch_quant_int8(const RowsInt8& a, int dtype, int num_sms, cudaStream_t st) {
   if (a.M == 0) return cudaSuccess;
-  if (dtype == 0) return rows_dispatch<kI8Plain, __nv_bfloat16>(a, st);
-  if (dtype == 1) return rows_dispatch<kI8Plain, __half>(a, st);
-  return rows_dispatch<kI8Plain, float>(a, st);
+  if (dtype == 0) return rows_dispatch<kI8Plain, __nv_bfloat16>(a, num_sms, st);
+  if (dtype == 1) return rows_dispatch<kI8Plain, __half>(a, num_sms, st);
+  return rows_dispatch<kI8Plain, float>(a, num_sms, st);
 }
 cudaError_t launch_ln_quant_int8(const RowsInt8& a, int num_sms, cudaStream_t st) {
   if (a.M == 0) return cudaSuccess;
   const int chunks = (a.K + 7) / 8;
-  if (rows_aligned<__nv_bfloat16>(a)) {
-    if (chunks <= 160) return ln_rows_launch<32, 5>(a, num_sms, st);
-    if (chunks <= 256) return ln_rows_launch<32, 8>(a, num_sms, st);
-    if (chunks <= 640) return ln_rows_launch<128, 5>(a, num_sms, st);
-    if (chunks <= 1024) return ln_rows_launch<128, 8>(a, num_sms, st);
-  }
+  if (chunks <= 144) return ln_rows_launch<16>(a, num_sms, st);
+  if (chunks <= 256) return ln_rows_launch<32>(a, num_sms, st);
+  if (chunks <= 2048) return ln_rows_launch<128>(a, num_sms, st);
   return rows_any_launch<kI8Ln, __nv_bfloat16>(a, st);
 }
-cudaError_t launch_gelu_quant_int8(const RowsInt8& a, cudaStream_t st) {
-  return a.M == 0 ? cudaSuccess : rows_dispatch<kI8Gelu, __nv_bfloat16>(a, st);
+cudaError_t launch_gelu_quant_int8(const RowsInt8& a, int num_sms, cudaStream_t st) {
+  return a.M == 0 ? cudaSuccess : rows_dispatch<kI8Gelu, __nv_bfloat16>(a, num_sms, st);
 }
 
 }  // namespace vitq

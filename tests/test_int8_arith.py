@@ -24,8 +24,7 @@ def _codes(y, amax):
     side = 0.5 * amax - 63.5 * s.astype(np.float64)       # exact in fp64: its sign is the FMA's
     r64 = r.astype(np.float64)
     r = np.where(side > 0, r64 * (1 + 2.0 ** -21), np.where(side < 0, r64 * (1 - 2.0 ** -21), r64)).astype(f)
-    p = (y.astype(f) * r).astype(f)
-    k = (p + f(12582912.0)).astype(f) - f(12582912.0)     # nearest integer, ties to even
+    k = np.rint(y * r.astype(np.float64))                 # the exact product (32 bits), rounded half to even by the FMA
     return k.astype(np.int64), s
 
 
