@@ -52,12 +52,16 @@ __device__ __forceinline__ uint4 pack16(const float* v) {
 }
 
 // ------------------------------------------------------------------ tiles
-template <int BN>
+// kPair: two CTAs (cta_group::2) share one 256 x BN tile: each holds 128 rows of A, half
+// of the W rows, and the accumulator of its own 128 rows.
+template <int BN, bool kPair>
 struct I8Cfg {
   static constexpr int BM = 128, BK = 128;   // 128 codes = one 128B swizzle row
-  static constexpr int STAGES = BN == 256 ? 3 : 5;
+  static constexpr int TILE_M = kPair ? 256 : 128;
+  static constexpr int B_ROWS = kPair ? BN / 2 : BN;
+  static constexpr int STAGES = BN == 256 && !kPair ? 3 : 5;
   static constexpr int A_BYTES = BM * BK;
-  static constexpr int B_BYTES = BN * BK;
+  static constexpr int B_BYTES = B_ROWS * BK;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
   static constexpr int NACC = 2;              // TMEM accumulators, alternating between tiles
   static constexpr int EPI_WARPS = 4, EPI_WARP0 = 4;
@@ -70,9 +74,9 @@ struct I8Cfg {
   static constexpr size_t SMEM = (size_t)STAGES * STAGE_BYTES + OUT_BYTES + COL_BYTES + 1024 + BAR_BYTES;
 };
 
-template <int BN>
+template <int BN, bool kPair>
 struct I8Smem {
-  using Cfg = I8Cfg<BN>;
+  using Cfg = I8Cfg<BN, kPair>;
   uint8_t* base;
   __device__ uint32_t a(int s) const { return smem_u32(base + (size_t)s * Cfg::STAGE_BYTES); }
   __device__ uint32_t b(int s) const { return a(s) + Cfg::A_BYTES; }
@@ -101,20 +105,29 @@ __device__ __forceinline__ void i8_tile_coords(int tile, int tiles_m, int tiles_
   n = (tile / tiles_m + m) % tiles_n;
 }
 
-template <int BN>
-__device__ void i8_producer(const I8Smem<BN>& sm, const CUtensorMap* tmA, const CUtensorMap* tmB, int tiles_m,
-                            int tiles_n, int num_tiles, int nkb) {
-  using Cfg = I8Cfg<BN>;
+// Tiles of this CTA (or pair): t0, t0 + dt, ...
+template <int BN, bool kPair>
+__device__ void i8_producer(const I8Smem<BN, kPair>& sm, const CUtensorMap* tmA, const CUtensorMap* tmB, int tiles_m,
+                            int tiles_n, int num_tiles, int nkb, int t0, int dt, int rank) {
+  using Cfg = I8Cfg<BN, kPair>;
   int stage = 0;
   uint32_t phase = 0;
-  for (int tile = blockIdx.x; tile < num_tiles; tile += gridDim.x) {
+  for (int tile = t0; tile < num_tiles; tile += dt) {
     int mt, nt;
     i8_tile_coords(tile, tiles_m, tiles_n, mt, nt);
+    const int m0 = mt * Cfg::TILE_M + rank * Cfg::BM, n0 = nt * BN + rank * Cfg::B_ROWS;
     for (int kb = 0; kb < nkb; ++kb) {
       if (!mbar_wait(sm.empty(stage), phase ^ 1u, sm.abort_flag())) return;
-      mbar_arrive_expect_tx(sm.full(stage), Cfg::STAGE_BYTES);
-      tma_load_2d(sm.a(stage), tmA, kb * Cfg::BK, mt * Cfg::BM, sm.full(stage));
-      tma_load_2d(sm.b(stage), tmB, kb * Cfg::BK, nt * BN, sm.full(stage));
+      if (kPair) {   // both CTAs' copies count on the leader's barrier, which expects them all
+        const uint32_t full0 = mapa_shared(sm.full(stage), 0);
+        if (rank == 0) mbar_arrive_expect_tx(sm.full(stage), 2 * Cfg::STAGE_BYTES);
+        tma_load_2d_pair(sm.a(stage), tmA, kb * Cfg::BK, m0, full0);
+        tma_load_2d_pair(sm.b(stage), tmB, kb * Cfg::BK, n0, full0);
+      } else {
+        mbar_arrive_expect_tx(sm.full(stage), Cfg::STAGE_BYTES);
+        tma_load_2d(sm.a(stage), tmA, kb * Cfg::BK, m0, sm.full(stage));
+        tma_load_2d(sm.b(stage), tmB, kb * Cfg::BK, n0, sm.full(stage));
+      }
       if (++stage == Cfg::STAGES) {
         stage = 0;
         phase ^= 1u;
@@ -123,13 +136,13 @@ __device__ void i8_producer(const I8Smem<BN>& sm, const CUtensorMap* tmA, const 
   }
 }
 
-template <int BN>
-__device__ void i8_mma(const I8Smem<BN>& sm, uint32_t tmem_base, int num_tiles, int nkb, int K) {
-  using Cfg = I8Cfg<BN>;
-  constexpr uint32_t idesc = make_idesc_i8(128, BN);
+template <int BN, bool kPair>
+__device__ void i8_mma(const I8Smem<BN, kPair>& sm, uint32_t tmem_base, int num_tiles, int nkb, int K, int t0, int dt) {
+  using Cfg = I8Cfg<BN, kPair>;
+  constexpr uint32_t idesc = make_idesc_i8(Cfg::TILE_M, BN);
   int stage = 0;
   uint32_t phase = 0, it = 0;
-  for (int tile = blockIdx.x; tile < num_tiles; tile += gridDim.x, ++it) {
+  for (int tile = t0; tile < num_tiles; tile += dt, ++it) {
     const uint32_t acc = it % Cfg::NACC;
     if (!mbar_wait(sm.tempty(acc), ((it / Cfg::NACC) & 1u) ^ 1u, sm.abort_flag())) return;
     tc_fence_after();
@@ -138,24 +151,37 @@ __device__ void i8_mma(const I8Smem<BN>& sm, uint32_t tmem_base, int num_tiles, 
       tc_fence_after();
       const uint32_t a0 = sm.a(stage), b0 = sm.b(stage);
 #pragma unroll
-      for (int k = 0; k < 4; ++k)   // 32 codes each; steps that lie past K hold zeros and are left out
-        if (kb * Cfg::BK + 32 * k < K)
-          mma_i8_ss(tmem_base + acc * BN, make_smem_desc(a0 + 32 * k, 16, 1024, kSwizzle128B),
-                    make_smem_desc(b0 + 32 * k, 16, 1024, kSwizzle128B), idesc, (kb > 0 || k > 0) ? 1u : 0u);
-      tc_commit(sm.empty(stage));
+      for (int k = 0; k < 4; ++k) {   // 32 codes each; steps that lie past K hold zeros and are left out
+        if (kb * Cfg::BK + 32 * k >= K) break;
+        const uint64_t ad = make_smem_desc(a0 + 32 * k, 16, 1024, kSwizzle128B);
+        const uint64_t bd = make_smem_desc(b0 + 32 * k, 16, 1024, kSwizzle128B);
+        if (kPair)
+          mma_i8_ss_pair(tmem_base + acc * BN, ad, bd, idesc, (kb > 0 || k > 0) ? 1u : 0u);
+        else
+          mma_i8_ss(tmem_base + acc * BN, ad, bd, idesc, (kb > 0 || k > 0) ? 1u : 0u);
+      }
+      if (kPair)
+        tc_commit_pair(sm.empty(stage), 0x3);
+      else
+        tc_commit(sm.empty(stage));
       if (++stage == Cfg::STAGES) {
         stage = 0;
         phase ^= 1u;
       }
     }
-    tc_commit(sm.tfull(acc));
+    if (kPair)
+      tc_commit_pair(sm.tfull(acc), 0x3);
+    else
+      tc_commit(sm.tfull(acc));
   }
 }
 
-template <int BN, class T>
-__device__ void i8_epilogue(const I8Smem<BN>& sm, uint32_t tmem_base, const I8Args& g, const CUtensorMap* tmC,
-                            int tiles_m, int tiles_n, int num_tiles) {
-  using Cfg = I8Cfg<BN>;
+template <int BN, bool kPair, class T>
+__device__ void i8_epilogue(const I8Smem<BN, kPair>& sm, uint32_t tmem_base, const I8Args& g, const CUtensorMap* tmC,
+                            int tiles_m, int tiles_n, int num_tiles, int t0, int dt, int rank) {
+  using Cfg = I8Cfg<BN, kPair>;
+  // the leader's tempty barriers count both CTAs' epilogue warps
+  const uint32_t tempty0 = kPair ? mapa_shared(sm.tempty(0), 0) : sm.tempty(0);
   constexpr int PER = 16 / (int)sizeof(T);          // elements per 16 bytes
   constexpr int BOXC = 128 / (int)sizeof(T);        // columns per box
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -165,10 +191,10 @@ __device__ void i8_epilogue(const I8Smem<BN>& sm, uint32_t tmem_base, const I8Ar
   const T* bias = reinterpret_cast<const T*>(g.bias);
   const T* res = reinterpret_cast<const T*>(g.residual);
   uint32_t it = 0, box = 0;
-  for (int tile = blockIdx.x; tile < num_tiles; tile += gridDim.x, ++it) {
+  for (int tile = t0; tile < num_tiles; tile += dt, ++it) {
     int mt, nt;
     i8_tile_coords(tile, tiles_m, tiles_n, mt, nt);
-    const int col0 = nt * BN, y0 = mt * Cfg::BM + quad * 32, row = y0 + lane;
+    const int col0 = nt * BN, y0 = mt * Cfg::TILE_M + rank * Cfg::BM + quad * 32, row = y0 + lane;
     const uint32_t acc = it % Cfg::NACC;
     __syncwarp();
     for (int c = lane; c < BN; c += 32) {
@@ -250,25 +276,33 @@ __device__ void i8_epilogue(const I8Smem<BN>& sm, uint32_t tmem_base, const I8Ar
     }
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) mbar_arrive(sm.tempty(acc));
+    if (lane == 0) {
+      if (kPair)
+        mbar_arrive_cluster(tempty0 + acc * 8);
+      else
+        mbar_arrive(sm.tempty(acc));
+    }
   }
   if (lane == 0) bulk_wait_all();
 }
 
-template <int BN, class T>
-__global__ void __launch_bounds__(I8Cfg<BN>::THREADS, 1)
+template <int BN, bool kPair, class T>
+__global__ void __launch_bounds__(I8Cfg<BN, kPair>::THREADS, 1)
     int8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                      const __grid_constant__ CUtensorMap tmC, const I8Args args) {
-  using Cfg = I8Cfg<BN>;
+  using Cfg = I8Cfg<BN, kPair>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   pdl_trigger();
-  I8Smem<BN> sm;
+  I8Smem<BN, kPair> sm;
   sm.base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int nkb = (args.K + Cfg::BK - 1) / Cfg::BK;
-  const int tiles_m = (args.M + Cfg::BM - 1) / Cfg::BM;
+  const int tiles_m = (args.M + Cfg::TILE_M - 1) / Cfg::TILE_M;
   const int tiles_n = (args.N + BN - 1) / BN;
   const int num_tiles = tiles_m * tiles_n;
+  const int rank = kPair ? (int)cluster_ctarank() : 0;
+  const int t0 = kPair ? (int)blockIdx.x / 2 : (int)blockIdx.x;
+  const int dt = kPair ? (int)gridDim.x / 2 : (int)gridDim.x;
   if (threadIdx.x == 0) {
     for (int s = 0; s < Cfg::STAGES; ++s) {
       mbar_init(sm.full(s), 1);
@@ -276,14 +310,20 @@ __global__ void __launch_bounds__(I8Cfg<BN>::THREADS, 1)
     }
     for (int b = 0; b < Cfg::NACC; ++b) {
       mbar_init(sm.tfull(b), 1);
-      mbar_init(sm.tempty(b), Cfg::EPI_WARPS);
+      mbar_init(sm.tempty(b), Cfg::EPI_WARPS * (kPair ? 2 : 1));
     }
     *sm.abort_flag() = 0;
     fence_barrier_init();
   }
+  if (kPair) cluster_sync_all();   // the peer's barriers exist before anything signals them
   if (warp == 1) {
-    tmem_alloc(smem_u32(sm.tmem_holder()), 512);
-    tmem_relinquish();
+    if (kPair) {
+      tmem_alloc_pair(smem_u32(sm.tmem_holder()), 512);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(smem_u32(sm.tmem_holder()), 512);
+      tmem_relinquish();
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -292,26 +332,31 @@ __global__ void __launch_bounds__(I8Cfg<BN>::THREADS, 1)
   const uint32_t tmem_base = *sm.tmem_holder();
   if (warp < Cfg::EPI_WARP0) {
     if (warp == 0 && lane == 0) {
-      i8_producer<BN>(sm, &tmA, &tmB, tiles_m, tiles_n, num_tiles, nkb);
-    } else if (warp == 1 && lane == 0) {
-      i8_mma<BN>(sm, tmem_base, num_tiles, nkb, args.K);
+      i8_producer<BN, kPair>(sm, &tmA, &tmB, tiles_m, tiles_n, num_tiles, nkb, t0, dt, rank);
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+      i8_mma<BN, kPair>(sm, tmem_base, num_tiles, nkb, args.K, t0, dt);
     }
   } else {
-    i8_epilogue<BN, T>(sm, tmem_base, args, &tmC, tiles_m, tiles_n, num_tiles);
+    i8_epilogue<BN, kPair, T>(sm, tmem_base, args, &tmC, tiles_m, tiles_n, num_tiles, t0, dt, rank);
   }
   tc_fence_before();
   __syncthreads();
   if (*sm.abort_flag()) settle_pause(50000);
+  // neither CTA of a pair leaves while the leader's MMAs may still use the peer's memory
+  if (kPair) cluster_sync_all();
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc(tmem_base, 512);
+    if (kPair)
+      tmem_dealloc_pair(tmem_base, 512);
+    else
+      tmem_dealloc(tmem_base, 512);
   }
 }
 
-template <int BN, class T>
+template <int BN, bool kPair, class T>
 cudaError_t i8_launch(const Int8Gemm& p, int num_sms, cudaStream_t st) {
-  using Cfg = I8Cfg<BN>;
+  using Cfg = I8Cfg<BN, kPair>;
   constexpr int es = (int)sizeof(T);
   I8Args a{p.sA, p.sW, p.bias, p.residual, p.C, p.ldr, p.ldc, p.M, p.N, p.K, 0, 0};
   a.c_tma = (reinterpret_cast<uintptr_t>(p.C) & 15u) == 0 && ((size_t)p.ldc * es) % 16 == 0;
@@ -319,7 +364,7 @@ cudaError_t i8_launch(const Int8Gemm& p, int num_sms, cudaStream_t st) {
   CUtensorMap tmA, tmB, tmC;
   cudaError_t e = encode_tma_2d_ld(&tmA, 1, p.A, p.K, p.M, (size_t)p.lda, 128, 128);
   if (e != cudaSuccess) return e;
-  e = encode_tma_2d_ld(&tmB, 1, p.W, p.K, p.N, (size_t)p.ldw, 128, BN);
+  e = encode_tma_2d_ld(&tmB, 1, p.W, p.K, p.N, (size_t)p.ldw, 128, Cfg::B_ROWS);
   if (e != cudaSuccess) return e;
   if (a.c_tma) {
     e = encode_tma_2d_ld(&tmC, es, p.C, p.N, p.M, (size_t)p.ldc * es, 128 / es, 32);
@@ -327,16 +372,20 @@ cudaError_t i8_launch(const Int8Gemm& p, int num_sms, cudaStream_t st) {
   } else {
     tmC = tmA;   // not used
   }
-  e = cudaFuncSetAttribute(int8_gemm_kernel<BN, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg::SMEM);
+  auto kern = int8_gemm_kernel<BN, kPair, T>;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg::SMEM);
   if (e != cudaSuccess) return e;
-  const long long tiles = (long long)((p.M + Cfg::BM - 1) / Cfg::BM) * ((p.N + BN - 1) / BN);
-  const int grid = tiles < num_sms ? (int)tiles : num_sms;
-  return launch_pdl(int8_gemm_kernel<BN, T>, dim3(grid), dim3(Cfg::THREADS), Cfg::SMEM, st, tmA, tmB, tmC, a);
+  const long long tiles = (long long)((p.M + Cfg::TILE_M - 1) / Cfg::TILE_M) * ((p.N + BN - 1) / BN);
+  const int units = kPair ? num_sms / 2 : num_sms;
+  const int grid = tiles < units ? (int)tiles : units;
+  return kPair ? launch_pdl_pair(kern, dim3(2 * grid), dim3(Cfg::THREADS), Cfg::SMEM, st, tmA, tmB, tmC, a)
+               : launch_pdl(kern, dim3(grid), dim3(Cfg::THREADS), Cfg::SMEM, st, tmA, tmB, tmC, a);
 }
 
 template <class T>
 cudaError_t i8_pick(const Int8Gemm& p, int num_sms, cudaStream_t st) {
-  return p.N > 128 ? i8_launch<256, T>(p, num_sms, st) : i8_launch<128, T>(p, num_sms, st);
+  if (p.M > 1024 && p.N > 128) return i8_launch<256, true, T>(p, num_sms, st);
+  return p.N > 128 ? i8_launch<256, false, T>(p, num_sms, st) : i8_launch<128, false, T>(p, num_sms, st);
 }
 
 }  // namespace
