@@ -21,8 +21,9 @@ struct I8Args {
   const void* residual;
   void* C;
   int ldr, ldc, M, N, K;
-  int c_tma;     // C can be written by TMA (16-byte aligned base and row pitch)
-  int r_vec;     // residual can be read 16 bytes at a time
+  // how a 32-row box of C leaves and one of the residual arrives: by TMA (16-byte aligned
+  // base and row pitch), or by the warp in words of this many bytes (4, or 2)
+  int c_tma, r_tma, c_word, r_word;
 };
 
 // ------------------------------------------------------------------ output types
@@ -59,18 +60,19 @@ struct I8Cfg {
   static constexpr int BM = 128, BK = 128;   // 128 codes = one 128B swizzle row
   static constexpr int TILE_M = kPair ? 256 : 128;
   static constexpr int B_ROWS = kPair ? BN / 2 : BN;
-  static constexpr int STAGES = BN == 256 && !kPair ? 3 : 5;
+  static constexpr int STAGES = BN == 256 && !kPair ? 3 : 4;
   static constexpr int A_BYTES = BM * BK;
   static constexpr int B_BYTES = B_ROWS * BK;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
   static constexpr int NACC = 2;              // TMEM accumulators, alternating between tiles
-  static constexpr int EPI_WARPS = 4, EPI_WARP0 = 4;
-  static constexpr int THREADS = 256;
+  static constexpr int EPI_WARPS = 8, EPI_WARP0 = 4;   // a row quadrant and half of the columns each
+  static constexpr int COLS = BN / 2;                  // columns of an epilogue warp
+  static constexpr int THREADS = 32 * (EPI_WARP0 + EPI_WARPS);
   static constexpr int BOX_BYTES = 4096;      // 32 rows x 128 bytes of C
   static constexpr int BOXES = 2;             // per epilogue warp
   static constexpr int OUT_BYTES = EPI_WARPS * BOXES * BOX_BYTES;
-  static constexpr int COL_BYTES = EPI_WARPS * BN * 8;   // (sW, bias) per column, a copy per warp
-  static constexpr int BAR_BYTES = (2 * STAGES + 2 * NACC) * 8 + 16;
+  static constexpr int COL_BYTES = EPI_WARPS * COLS * 8;   // sW, then bias, of the warp's columns
+  static constexpr int BAR_BYTES = (2 * STAGES + 2 * NACC + EPI_WARPS * BOXES) * 8 + 16;
   static constexpr size_t SMEM = (size_t)STAGES * STAGE_BYTES + OUT_BYTES + COL_BYTES + 1024 + BAR_BYTES;
 };
 
@@ -83,8 +85,8 @@ struct I8Smem {
   __device__ uint8_t* out(int w) const {
     return base + (size_t)Cfg::STAGES * Cfg::STAGE_BYTES + (size_t)w * Cfg::BOXES * Cfg::BOX_BYTES;
   }
-  __device__ float2* cols(int w) const {
-    return reinterpret_cast<float2*>(base + (size_t)Cfg::STAGES * Cfg::STAGE_BYTES + Cfg::OUT_BYTES) + w * BN;
+  __device__ float* cols(int w) const {
+    return reinterpret_cast<float*>(base + (size_t)Cfg::STAGES * Cfg::STAGE_BYTES + Cfg::OUT_BYTES) + w * 2 * Cfg::COLS;
   }
   __device__ uint64_t* bars() const {
     return reinterpret_cast<uint64_t*>(base + (size_t)Cfg::STAGES * Cfg::STAGE_BYTES + Cfg::OUT_BYTES + Cfg::COL_BYTES);
@@ -93,8 +95,11 @@ struct I8Smem {
   __device__ uint32_t empty(int s) const { return smem_u32(bars() + Cfg::STAGES + s); }
   __device__ uint32_t tfull(int b) const { return smem_u32(bars() + 2 * Cfg::STAGES + b); }
   __device__ uint32_t tempty(int b) const { return smem_u32(bars() + 2 * Cfg::STAGES + Cfg::NACC + b); }
+  __device__ uint32_t res_full(int w, int slot) const {
+    return smem_u32(bars() + 2 * Cfg::STAGES + 2 * Cfg::NACC + w * Cfg::BOXES + slot);
+  }
   __device__ uint32_t* tmem_holder() const {
-    return reinterpret_cast<uint32_t*>(bars() + 2 * Cfg::STAGES + 2 * Cfg::NACC);
+    return reinterpret_cast<uint32_t*>(bars() + 2 * Cfg::STAGES + 2 * Cfg::NACC + Cfg::EPI_WARPS * Cfg::BOXES);
   }
   __device__ volatile int* abort_flag() const { return reinterpret_cast<volatile int*>(tmem_holder() + 1); }
 };
@@ -176,104 +181,176 @@ __device__ void i8_mma(const I8Smem<BN, kPair>& sm, uint32_t tmem_base, int num_
   }
 }
 
+// Byte b of row r of a box of 32 rows x 128 bytes (TMA's 128-byte swizzle).
+__device__ __forceinline__ int box_at(int r, int b) { return r * 128 + (b ^ ((r & 7) << 4)); }
+
+// A box between shared memory and rows of any alignment, word by word: lanes along the
+// row, so that each access of the warp is one run of 128 (or 64) bytes.  rows, bytes:
+// what of the box lies inside the matrix.
+template <class W, bool kStore>
+__device__ __forceinline__ void box_words(uint8_t* slot, uint8_t* mat, size_t pitch, int rows, int bytes) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int b = lane * (int)sizeof(W); b < 128; b += 32 * (int)sizeof(W)) {
+    if (b < bytes) {
+      W v[32];   // all in flight at once
+#pragma unroll
+      for (int r = 0; r < 32; ++r)
+        if (r < rows) v[r] = kStore ? *reinterpret_cast<W*>(slot + box_at(r, b)) : *reinterpret_cast<W*>(mat + r * pitch + b);
+#pragma unroll
+      for (int r = 0; r < 32; ++r)
+        if (r < rows) *reinterpret_cast<W*>(kStore ? mat + r * pitch + b : slot + box_at(r, b)) = v[r];
+    }
+  }
+}
+
+// Epilogue warp: 32 rows (thread = row) and COLS columns, 32 columns at a time; the next
+// 32 columns' accumulators are on their way while the present ones are scaled.  Each
+// 128-byte-wide box of C has one of two slots in shared memory: the residual is brought
+// there first (for the first two boxes of a tile while its sum is still running), the
+// finished box leaves from there.
 template <int BN, bool kPair, class T>
 __device__ void i8_epilogue(const I8Smem<BN, kPair>& sm, uint32_t tmem_base, const I8Args& g, const CUtensorMap* tmC,
-                            int tiles_m, int tiles_n, int num_tiles, int t0, int dt, int rank) {
+                            const CUtensorMap* tmR, int tiles_m, int tiles_n, int num_tiles, int t0, int dt, int rank) {
   using Cfg = I8Cfg<BN, kPair>;
-  // the leader's tempty barriers count both CTAs' epilogue warps
-  const uint32_t tempty0 = kPair ? mapa_shared(sm.tempty(0), 0) : sm.tempty(0);
   constexpr int PER = 16 / (int)sizeof(T);          // elements per 16 bytes
   constexpr int BOXC = 128 / (int)sizeof(T);        // columns per box
+  constexpr int GROUPS = Cfg::COLS / 32, PER_BOX = BOXC / 32, NBOX = Cfg::COLS / BOXC;
+  // the leader's tempty barriers count both CTAs' epilogue warps
+  const uint32_t tempty0 = kPair ? mapa_shared(sm.tempty(0), 0) : sm.tempty(0);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int ew = warp - Cfg::EPI_WARP0, quad = warp & 3;
+  const int ew = warp - Cfg::EPI_WARP0, quad = warp & 3, half = ew >> 2;
   uint8_t* stg = sm.out(ew);
-  float2* cols = sm.cols(ew);
+  float* sw_s = sm.cols(ew);
+  float* bias_s = sw_s + Cfg::COLS;
   const T* bias = reinterpret_cast<const T*>(g.bias);
-  const T* res = reinterpret_cast<const T*>(g.residual);
-  uint32_t it = 0, box = 0;
+  const bool has_res = g.residual != nullptr;
+  uint32_t it = 0, slot_it = 0, res_phase = 0;   // boxes so far; phase of each slot's residual barrier
   for (int tile = t0; tile < num_tiles; tile += dt, ++it) {
     int mt, nt;
     i8_tile_coords(tile, tiles_m, tiles_n, mt, nt);
-    const int col0 = nt * BN, y0 = mt * Cfg::TILE_M + rank * Cfg::BM + quad * 32, row = y0 + lane;
+    const int col0 = nt * BN + half * Cfg::COLS;
+    const int y0 = mt * Cfg::TILE_M + rank * Cfg::BM + quad * 32, row = y0 + lane;
     const uint32_t acc = it % Cfg::NACC;
-    __syncwarp();
-    for (int c = lane; c < BN; c += 32) {
-      const int n = col0 + c;
-      cols[c] = n < g.N ? make_float2(__ldg(g.sW + n), bias ? to_f32<T>(bias[n]) : 0.f) : make_float2(0.f, 0.f);
-    }
-    const float sa = row < g.M ? __ldg(g.sA + row) : 0.f;
-    __syncwarp();
-    const bool ok = mbar_wait(sm.tfull(acc), (it / Cfg::NACC) & 1u, sm.abort_flag());
-    if (!__all_sync(0xffffffffu, ok)) return;
-    tc_fence_after();
-    const uint32_t taddr = tmem_base + ((uint32_t)(quad * 32) << 16) + acc * BN;
-#pragma unroll 1
-    for (int c0 = 0; c0 < BN; c0 += BOXC) {
-      if (col0 + c0 >= g.N) break;
-      uint8_t* slot = stg + (box & 1u) * Cfg::BOX_BYTES;
-      if (g.c_tma) {   // the store before last has read its box
-        if (lane == 0) bulk_wait_read<1>();
+    const int groups = y0 < g.M ? min(GROUPS, (g.N - col0 + 31) >> 5) : 0;   // groups inside C (may be < 0)
+    const int nbox = (groups + PER_BOX - 1) / PER_BOX;
+    const int rows = min(32, g.M - y0);
+    // brings the residual of box b of this tile to its slot, once the slot's last store has read it
+    auto fetch_res = [&](int b) {
+      uint8_t* slot = stg + ((slot_it + b) & 1u) * Cfg::BOX_BYTES;
+      const int c0 = col0 + b * BOXC;
+      if (g.r_tma) {
+        fence_proxy_async_smem();   // the warp's own accesses to the slot come before the copy
+        __syncwarp();
+        if (lane == 0) {
+          const uint32_t bar = sm.res_full(ew, (slot_it + b) & 1u);
+          mbar_arrive_expect_tx(bar, Cfg::BOX_BYTES);
+          tma_load_2d(smem_u32(slot), tmR, c0, y0, bar);
+        }
+      } else {
+        uint8_t* mat = const_cast<uint8_t*>(reinterpret_cast<const uint8_t*>(g.residual)) +
+                       ((size_t)y0 * g.ldr + c0) * sizeof(T);
+        const int bytes = min(128, (g.N - c0) * (int)sizeof(T));
+        if (g.r_word == 4) box_words<uint32_t, false>(slot, mat, (size_t)g.ldr * sizeof(T), rows, bytes);
+        else box_words<uint16_t, false>(slot, mat, (size_t)g.ldr * sizeof(T), rows, bytes);
         __syncwarp();
       }
+    };
+    if (has_res && nbox > 0) {
+      if (lane == 0) bulk_wait_read_all();
+      __syncwarp();
+      fetch_res(0);
+      if (nbox > 1) fetch_res(1);
+    }
+    __syncwarp();
 #pragma unroll
-      for (int h = 0; h < BOXC; h += 32) {
-        uint32_t r[32];
-        tmem_ld32(taddr + c0 + h, r);
-        uint4 ru[32 / PER];
-        const int colb = col0 + c0 + h;
-        if (res) {
+    for (int c = lane; c < Cfg::COLS; c += 32) {
+      const int n = col0 + c;
+      sw_s[c] = n < g.N ? __ldg(g.sW + n) : 0.f;
+      bias_s[c] = bias && n < g.N ? to_f32<T>(bias[n]) : 0.f;
+    }
+    const float sa = row < g.M ? __ldg(g.sA + row) : 0.f;
+    const uint64_t sa2 = f2pack(sa, sa);
+    __syncwarp();
+    bool ok = mbar_wait(sm.tfull(acc), (it / Cfg::NACC) & 1u, sm.abort_flag());
+    if (!__all_sync(0xffffffffu, ok)) return;
+    tc_fence_after();
+    const uint32_t taddr = tmem_base + ((uint32_t)(quad * 32) << 16) + acc * BN + half * Cfg::COLS;
+    uint32_t r[2][32];
+    if (groups > 0) tmem_ld32(taddr, r[0]);
 #pragma unroll
-          for (int c = 0; c < 32 / PER; ++c) {
-            const int col = colb + c * PER;
-            ru[c] = make_uint4(0u, 0u, 0u, 0u);
-            if (row < g.M) {
-              const T* p = res + (size_t)row * g.ldr + col;
-              if (g.r_vec && col + PER <= g.N) {
-                ru[c] = *reinterpret_cast<const uint4*>(p);
-              } else {
+    for (int b = 0; b < NBOX; ++b) {
+      if (b < nbox) {   // uniform
+        const uint32_t s = (slot_it + b) & 1u;
+        uint8_t* slot = stg + s * Cfg::BOX_BYTES;
+        if (has_res) {
+          if (g.r_tma) {
+            ok = mbar_wait(sm.res_full(ew, s), (res_phase >> s) & 1u, sm.abort_flag());
+            if (!__all_sync(0xffffffffu, ok)) return;
+            res_phase ^= 1u << s;
+          }
+        } else if (g.c_tma) {   // the store before last has read its box
+          if (lane == 0) bulk_wait_read<1>();
+          __syncwarp();
+        }
 #pragma unroll
-                for (int i = 0; i < PER; ++i)
-                  if (col + i < g.N) reinterpret_cast<T*>(&ru[c])[i] = p[i];
+        for (int h = 0; h < PER_BOX; ++h) {
+          const int gr = b * PER_BOX + h;
+          if (gr < groups) {
+            tmem_wait_ld();
+            if (gr + 1 < groups) tmem_ld32(taddr + (gr + 1) * 32, r[(gr + 1) & 1]);
+#pragma unroll
+            for (int c = 0; c < 32 / PER; ++c) {
+              float v[PER];
+#pragma unroll
+              for (int i = 0; i < PER; i += 4) {
+                const int at = gr * 32 + c * PER + i;
+                const float4 w = *reinterpret_cast<const float4*>(sw_s + at);
+                const float4 bi = *reinterpret_cast<const float4*>(bias_s + at);
+                const uint32_t* a = r[gr & 1] + c * PER + i;
+                const float2 lo =
+                    f2unpack(ffma2(fmul2(f2pack(__int2float_rn((int)a[0]), __int2float_rn((int)a[1])), sa2),
+                                   f2pack(w.x, w.y), f2pack(bi.x, bi.y)));
+                const float2 hi =
+                    f2unpack(ffma2(fmul2(f2pack(__int2float_rn((int)a[2]), __int2float_rn((int)a[3])), sa2),
+                                   f2pack(w.z, w.w), f2pack(bi.z, bi.w)));
+                v[i] = lo.x;
+                v[i + 1] = lo.y;
+                v[i + 2] = hi.x;
+                v[i + 3] = hi.y;
               }
+              uint4* at = reinterpret_cast<uint4*>(slot + box_at(lane, h * 32 * (int)sizeof(T) + c * 16));
+              if (has_res) {
+                float rv[PER];
+                unpack16<T>(*at, rv);
+#pragma unroll
+                for (int i = 0; i < PER; ++i) v[i] += rv[i];
+              }
+              *at = pack16<T>(v);
             }
           }
         }
-        tmem_wait_ld();
-#pragma unroll
-        for (int c = 0; c < 32 / PER; ++c) {
-          float v[PER];
-#pragma unroll
-          for (int i = 0; i < PER; ++i) {
-            const float2 sb = cols[c0 + h + c * PER + i];
-            v[i] = __fmaf_rn(__int2float_rn((int)r[c * PER + i]) * sa, sb.x, sb.y);
+        const int c0 = col0 + b * BOXC;
+        if (g.c_tma) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {   // TMA clips rows past M and columns past N
+            tma_store_2d(tmC, smem_u32(slot), c0, y0);
+            bulk_commit_group();
+            if (has_res && b + 2 < nbox) bulk_wait_read<0>();
           }
-          if (res) {
-            float rv[PER];
-            unpack16<T>(ru[c], rv);
-#pragma unroll
-            for (int i = 0; i < PER; ++i) v[i] += rv[i];
-          }
-          if (g.c_tma) {
-            const int ch = (h * (int)sizeof(T)) / 16 + c;
-            *reinterpret_cast<uint4*>(slot + lane * 128 + ((ch ^ (lane & 7)) << 4)) = pack16<T>(v);
-          } else if (row < g.M) {
-            T* p = reinterpret_cast<T*>(g.C) + (size_t)row * g.ldc + colb + c * PER;
-#pragma unroll
-            for (int i = 0; i < PER; ++i)
-              if (colb + c * PER + i < g.N) p[i] = of_f32<T>(v[i]);
-          }
+        } else {
+          __syncwarp();
+          uint8_t* mat = reinterpret_cast<uint8_t*>(g.C) + ((size_t)y0 * g.ldc + c0) * sizeof(T);
+          const int bytes = min(128, (g.N - c0) * (int)sizeof(T));
+          if (g.c_word == 4) box_words<uint32_t, true>(slot, mat, (size_t)g.ldc * sizeof(T), rows, bytes);
+          else box_words<uint16_t, true>(slot, mat, (size_t)g.ldc * sizeof(T), rows, bytes);
         }
-      }
-      if (g.c_tma) {
-        fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) {
-          if (y0 < g.M) tma_store_2d(tmC, smem_u32(slot), col0 + c0, y0);
-          bulk_commit_group();
-        }
-        ++box;
+        if (has_res && b + 2 < nbox) fetch_res(b + 2);
       }
     }
+    if (nbox > 0) slot_it += nbox;
     tc_fence_before();
     __syncwarp();
     if (lane == 0) {
@@ -289,7 +366,8 @@ __device__ void i8_epilogue(const I8Smem<BN, kPair>& sm, uint32_t tmem_base, con
 template <int BN, bool kPair, class T>
 __global__ void __launch_bounds__(I8Cfg<BN, kPair>::THREADS, 1)
     int8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                     const __grid_constant__ CUtensorMap tmC, const I8Args args) {
+                     const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmR,
+                     const I8Args args) {
   using Cfg = I8Cfg<BN, kPair>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   pdl_trigger();
@@ -312,6 +390,8 @@ __global__ void __launch_bounds__(I8Cfg<BN, kPair>::THREADS, 1)
       mbar_init(sm.tfull(b), 1);
       mbar_init(sm.tempty(b), Cfg::EPI_WARPS * (kPair ? 2 : 1));
     }
+    for (int w = 0; w < Cfg::EPI_WARPS; ++w)
+      for (int b = 0; b < Cfg::BOXES; ++b) mbar_init(sm.res_full(w, b), 1);
     *sm.abort_flag() = 0;
     fence_barrier_init();
   }
@@ -337,7 +417,7 @@ __global__ void __launch_bounds__(I8Cfg<BN, kPair>::THREADS, 1)
       i8_mma<BN, kPair>(sm, tmem_base, num_tiles, nkb, args.K, t0, dt);
     }
   } else {
-    i8_epilogue<BN, kPair, T>(sm, tmem_base, args, &tmC, tiles_m, tiles_n, num_tiles, t0, dt, rank);
+    i8_epilogue<BN, kPair, T>(sm, tmem_base, args, &tmC, &tmR, tiles_m, tiles_n, num_tiles, t0, dt, rank);
   }
   tc_fence_before();
   __syncthreads();
@@ -358,28 +438,34 @@ template <int BN, bool kPair, class T>
 cudaError_t i8_launch(const Int8Gemm& p, int num_sms, cudaStream_t st) {
   using Cfg = I8Cfg<BN, kPair>;
   constexpr int es = (int)sizeof(T);
-  I8Args a{p.sA, p.sW, p.bias, p.residual, p.C, p.ldr, p.ldc, p.M, p.N, p.K, 0, 0};
-  a.c_tma = (reinterpret_cast<uintptr_t>(p.C) & 15u) == 0 && ((size_t)p.ldc * es) % 16 == 0;
-  a.r_vec = (reinterpret_cast<uintptr_t>(p.residual) & 15u) == 0 && ((size_t)p.ldr * es) % 16 == 0;
-  CUtensorMap tmA, tmB, tmC;
+  I8Args a{p.sA, p.sW, p.bias, p.residual, p.C, p.ldr, p.ldc, p.M, p.N, p.K, 0, 0, 0, 0};
+  // widest access that a base address, a row pitch and (word by word) the row's length allow
+  auto bytes = [&](const void* base, size_t pitch) {
+    const uintptr_t v = reinterpret_cast<uintptr_t>(base) | pitch;
+    return v % 16 == 0 ? 16 : (v | (size_t)p.N * es) % 4 == 0 ? 4 : 2;
+  };
+  const size_t pc = (size_t)p.ldc * es, pr = (size_t)p.ldr * es;
+  a.c_word = bytes(p.C, pc);
+  a.r_word = p.residual ? bytes(p.residual, pr) : 0;
+  a.c_tma = a.c_word == 16;
+  a.r_tma = a.r_word == 16;
+  CUtensorMap tmA, tmB, tmC, tmR;
   cudaError_t e = encode_tma_2d_ld(&tmA, 1, p.A, p.K, p.M, (size_t)p.lda, 128, 128);
   if (e != cudaSuccess) return e;
   e = encode_tma_2d_ld(&tmB, 1, p.W, p.K, p.N, (size_t)p.ldw, 128, Cfg::B_ROWS);
   if (e != cudaSuccess) return e;
-  if (a.c_tma) {
-    e = encode_tma_2d_ld(&tmC, es, p.C, p.N, p.M, (size_t)p.ldc * es, 128 / es, 32);
-    if (e != cudaSuccess) return e;
-  } else {
-    tmC = tmA;   // not used
-  }
+  tmC = tmR = tmA;   // where not used
+  if (a.c_tma) e = encode_tma_2d_ld(&tmC, es, p.C, p.N, p.M, pc, 128 / es, 32);
+  if (e == cudaSuccess && a.r_tma) e = encode_tma_2d_ld(&tmR, es, p.residual, p.N, p.M, pr, 128 / es, 32);
+  if (e != cudaSuccess) return e;
   auto kern = int8_gemm_kernel<BN, kPair, T>;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg::SMEM);
   if (e != cudaSuccess) return e;
   const long long tiles = (long long)((p.M + Cfg::TILE_M - 1) / Cfg::TILE_M) * ((p.N + BN - 1) / BN);
   const int units = kPair ? num_sms / 2 : num_sms;
   const int grid = tiles < units ? (int)tiles : units;
-  return kPair ? launch_pdl_pair(kern, dim3(2 * grid), dim3(Cfg::THREADS), Cfg::SMEM, st, tmA, tmB, tmC, a)
-               : launch_pdl(kern, dim3(grid), dim3(Cfg::THREADS), Cfg::SMEM, st, tmA, tmB, tmC, a);
+  return kPair ? launch_pdl_pair(kern, dim3(2 * grid), dim3(Cfg::THREADS), Cfg::SMEM, st, tmA, tmB, tmC, tmR, a)
+               : launch_pdl(kern, dim3(grid), dim3(Cfg::THREADS), Cfg::SMEM, st, tmA, tmB, tmC, tmR, a);
 }
 
 template <class T>
