@@ -11,6 +11,9 @@
 
 #include <cuda_fp16.h>
 
+#include <cmath>
+#include <type_traits>
+
 namespace vitq {
 namespace {
 
@@ -21,9 +24,9 @@ struct I8Args {
   const void* residual;
   void* C;
   int ldr, ldc, M, N, K;
-  // how a 32-row box of C leaves and one of the residual arrives: by TMA (16-byte aligned
-  // base and row pitch), or by the warp in words of this many bytes (4, or 2)
-  int c_tma, r_tma, c_word, r_word;
+  // whether boxes of C leave and of the residual arrive by TMA (16-byte aligned base and row
+  // pitch); otherwise the residual is read in words of r_word bytes (4, or 2)
+  int c_tma, r_tma, r_word;
 };
 
 // ------------------------------------------------------------------ output types
@@ -60,7 +63,7 @@ struct I8Cfg {
   static constexpr int BM = 128, BK = 128;   // 128 codes = one 128B swizzle row
   static constexpr int TILE_M = kPair ? 256 : 128;
   static constexpr int B_ROWS = kPair ? BN / 2 : BN;
-  static constexpr int STAGES = BN == 256 && !kPair ? 3 : 4;
+  static constexpr int STAGES = 4;
   static constexpr int A_BYTES = BM * BK;
   static constexpr int B_BYTES = B_ROWS * BK;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
@@ -187,19 +190,48 @@ __device__ __forceinline__ int box_at(int r, int b) { return r * 128 + (b ^ ((r 
 // A box between shared memory and rows of any alignment, word by word: lanes along the
 // row, so that each access of the warp is one run of 128 (or 64) bytes.  rows, bytes:
 // what of the box lies inside the matrix.
-template <class W, bool kStore>
-__device__ __forceinline__ void box_words(uint8_t* slot, uint8_t* mat, size_t pitch, int rows, int bytes) {
+template <class W>
+__device__ __noinline__ void box_load(uint8_t* slot, const uint8_t* mat, size_t pitch, int rows, int bytes) {
   const int lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (int b = lane * (int)sizeof(W); b < bytes; b += 32 * (int)sizeof(W)) {
+    W v[32];   // all in flight at once
 #pragma unroll
-  for (int b = lane * (int)sizeof(W); b < 128; b += 32 * (int)sizeof(W)) {
-    if (b < bytes) {
-      W v[32];   // all in flight at once
+    for (int r = 0; r < 32; ++r) v[r] = *reinterpret_cast<const W*>(mat + min(r, rows - 1) * pitch + b);
 #pragma unroll
-      for (int r = 0; r < 32; ++r)
-        if (r < rows) v[r] = kStore ? *reinterpret_cast<W*>(slot + box_at(r, b)) : *reinterpret_cast<W*>(mat + r * pitch + b);
+    for (int r = 0; r < 32; ++r) *reinterpret_cast<W*>(slot + box_at(r, b)) = v[r];
+  }
+}
+// A box to rows of any alignment: whole 16-byte units of the matrix, put together from two
+// units of the box (8 lanes a row, 4 rows at a time), then the elements before the first
+// and behind the last unit.  E: element type by size.
+template <class E>
+__device__ __noinline__ void box_store(const uint8_t* slot, uint8_t* mat, size_t pitch, int rows, int bytes) {
+  const int lane = threadIdx.x & 31, k = lane & 7;
+#pragma unroll 2
+  for (int r = lane >> 3; r < rows; r += 4) {
+    uint8_t* row = mat + r * pitch;
+    const int lead = (int)(-reinterpret_cast<uintptr_t>(row) & 15u);   // bytes before the first unit
+    const int at = lead + 16 * k, whole = bytes > lead ? (bytes - lead) & ~15 : 0;
+    if (at < lead + whole) {
+      uint32_t v[8];
+      *reinterpret_cast<uint4*>(v) = *reinterpret_cast<const uint4*>(slot + box_at(r, at & ~15));
+      // the unit behind the last is not read from (its bytes are shifted out when lead = 0)
+      *reinterpret_cast<uint4*>(v + 4) = *reinterpret_cast<const uint4*>(slot + box_at(r, min(at + 15, 127) & ~15));
 #pragma unroll
-      for (int r = 0; r < 32; ++r)
-        if (r < rows) *reinterpret_cast<W*>(kStore ? mat + r * pitch + b : slot + box_at(r, b)) = v[r];
+      for (int i = 0; i < 6; ++i) v[i] = lead & 8 ? v[i + 2] : v[i];
+#pragma unroll
+      for (int i = 0; i < 5; ++i) v[i] = lead & 4 ? v[i + 1] : v[i];
+      if (sizeof(E) == 2) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = lead & 2 ? __byte_perm(v[i], v[i + 1], 0x5432) : v[i];
+      }
+      *reinterpret_cast<uint4*>(row + at) = make_uint4(v[0], v[1], v[2], v[3]);
+    }
+    const int head = min(lead, bytes), edge = bytes - whole;   // bytes: [0, head) and [head + whole, bytes)
+    for (int e = k * (int)sizeof(E); e < edge; e += 8 * (int)sizeof(E)) {
+      const int b = e < head ? e : e + whole;
+      *reinterpret_cast<E*>(row + b) = *reinterpret_cast<const E*>(slot + box_at(r, b));
     }
   }
 }
@@ -209,7 +241,9 @@ __device__ __forceinline__ void box_words(uint8_t* slot, uint8_t* mat, size_t pi
 // 128-byte-wide box of C has one of two slots in shared memory: the residual is brought
 // there first (for the first two boxes of a tile while its sum is still running), the
 // finished box leaves from there.
-template <int BN, bool kPair, class T>
+// kWords: C or the residual may need word-by-word rows (a kernel of its own: the extra
+// paths spill registers, 6 % of a large product's time).
+template <int BN, bool kPair, bool kWords, class T>
 __device__ void i8_epilogue(const I8Smem<BN, kPair>& sm, uint32_t tmem_base, const I8Args& g, const CUtensorMap* tmC,
                             const CUtensorMap* tmR, int tiles_m, int tiles_n, int num_tiles, int t0, int dt, int rank) {
   using Cfg = I8Cfg<BN, kPair>;
@@ -239,7 +273,7 @@ __device__ void i8_epilogue(const I8Smem<BN, kPair>& sm, uint32_t tmem_base, con
     auto fetch_res = [&](int b) {
       uint8_t* slot = stg + ((slot_it + b) & 1u) * Cfg::BOX_BYTES;
       const int c0 = col0 + b * BOXC;
-      if (g.r_tma) {
+      if (!kWords || g.r_tma) {
         fence_proxy_async_smem();   // the warp's own accesses to the slot come before the copy
         __syncwarp();
         if (lane == 0) {
@@ -248,11 +282,10 @@ __device__ void i8_epilogue(const I8Smem<BN, kPair>& sm, uint32_t tmem_base, con
           tma_load_2d(smem_u32(slot), tmR, c0, y0, bar);
         }
       } else {
-        uint8_t* mat = const_cast<uint8_t*>(reinterpret_cast<const uint8_t*>(g.residual)) +
-                       ((size_t)y0 * g.ldr + c0) * sizeof(T);
+        const uint8_t* mat = reinterpret_cast<const uint8_t*>(g.residual) + ((size_t)y0 * g.ldr + c0) * sizeof(T);
         const int bytes = min(128, (g.N - c0) * (int)sizeof(T));
-        if (g.r_word == 4) box_words<uint32_t, false>(slot, mat, (size_t)g.ldr * sizeof(T), rows, bytes);
-        else box_words<uint16_t, false>(slot, mat, (size_t)g.ldr * sizeof(T), rows, bytes);
+        if (g.r_word == 4) box_load<uint32_t>(slot, mat, (size_t)g.ldr * sizeof(T), rows, bytes);
+        else box_load<uint16_t>(slot, mat, (size_t)g.ldr * sizeof(T), rows, bytes);
         __syncwarp();
       }
     };
@@ -284,12 +317,12 @@ __device__ void i8_epilogue(const I8Smem<BN, kPair>& sm, uint32_t tmem_base, con
         const uint32_t s = (slot_it + b) & 1u;
         uint8_t* slot = stg + s * Cfg::BOX_BYTES;
         if (has_res) {
-          if (g.r_tma) {
+          if (!kWords || g.r_tma) {
             ok = mbar_wait(sm.res_full(ew, s), (res_phase >> s) & 1u, sm.abort_flag());
             if (!__all_sync(0xffffffffu, ok)) return;
             res_phase ^= 1u << s;
           }
-        } else if (g.c_tma) {   // the store before last has read its box
+        } else if (!kWords || g.c_tma) {   // the store before last has read its box
           if (lane == 0) bulk_wait_read<1>();
           __syncwarp();
         }
@@ -331,7 +364,7 @@ __device__ void i8_epilogue(const I8Smem<BN, kPair>& sm, uint32_t tmem_base, con
           }
         }
         const int c0 = col0 + b * BOXC;
-        if (g.c_tma) {
+        if (!kWords || g.c_tma) {
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {   // TMA clips rows past M and columns past N
@@ -343,8 +376,7 @@ __device__ void i8_epilogue(const I8Smem<BN, kPair>& sm, uint32_t tmem_base, con
           __syncwarp();
           uint8_t* mat = reinterpret_cast<uint8_t*>(g.C) + ((size_t)y0 * g.ldc + c0) * sizeof(T);
           const int bytes = min(128, (g.N - c0) * (int)sizeof(T));
-          if (g.c_word == 4) box_words<uint32_t, true>(slot, mat, (size_t)g.ldc * sizeof(T), rows, bytes);
-          else box_words<uint16_t, true>(slot, mat, (size_t)g.ldc * sizeof(T), rows, bytes);
+          box_store<std::conditional_t<sizeof(T) == 2, uint16_t, uint32_t>>(slot, mat, (size_t)g.ldc * sizeof(T), rows, bytes);
         }
         __syncwarp();
         if (has_res && b + 2 < nbox) fetch_res(b + 2);
@@ -363,7 +395,7 @@ __device__ void i8_epilogue(const I8Smem<BN, kPair>& sm, uint32_t tmem_base, con
   if (lane == 0) bulk_wait_all();
 }
 
-template <int BN, bool kPair, class T>
+template <int BN, bool kPair, bool kWords, class T>
 __global__ void __launch_bounds__(I8Cfg<BN, kPair>::THREADS, 1)
     int8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                      const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmR,
@@ -417,7 +449,7 @@ __global__ void __launch_bounds__(I8Cfg<BN, kPair>::THREADS, 1)
       i8_mma<BN, kPair>(sm, tmem_base, num_tiles, nkb, args.K, t0, dt);
     }
   } else {
-    i8_epilogue<BN, kPair, T>(sm, tmem_base, args, &tmC, &tmR, tiles_m, tiles_n, num_tiles, t0, dt, rank);
+    i8_epilogue<BN, kPair, kWords, T>(sm, tmem_base, args, &tmC, &tmR, tiles_m, tiles_n, num_tiles, t0, dt, rank);
   }
   tc_fence_before();
   __syncthreads();
@@ -434,21 +466,25 @@ __global__ void __launch_bounds__(I8Cfg<BN, kPair>::THREADS, 1)
   }
 }
 
-template <int BN, bool kPair, class T>
-cudaError_t i8_launch(const Int8Gemm& p, int num_sms, cudaStream_t st) {
-  using Cfg = I8Cfg<BN, kPair>;
-  constexpr int es = (int)sizeof(T);
-  I8Args a{p.sA, p.sW, p.bias, p.residual, p.C, p.ldr, p.ldc, p.M, p.N, p.K, 0, 0, 0, 0};
+// How a box of C leaves and one of the residual arrives (I8Args).
+void i8_paths(const Int8Gemm& p, int es, I8Args* a) {
   // widest access that a base address, a row pitch and (word by word) the row's length allow
   auto bytes = [&](const void* base, size_t pitch) {
     const uintptr_t v = reinterpret_cast<uintptr_t>(base) | pitch;
     return v % 16 == 0 ? 16 : (v | (size_t)p.N * es) % 4 == 0 ? 4 : 2;
   };
+  a->c_tma = bytes(p.C, (size_t)p.ldc * es) == 16;
+  a->r_word = p.residual ? bytes(p.residual, (size_t)p.ldr * es) : 0;
+  a->r_tma = a->r_word == 16;
+}
+
+template <int BN, bool kPair, class T>
+cudaError_t i8_launch(const Int8Gemm& p, int num_sms, cudaStream_t st) {
+  using Cfg = I8Cfg<BN, kPair>;
+  constexpr int es = (int)sizeof(T);
+  I8Args a{p.sA, p.sW, p.bias, p.residual, p.C, p.ldr, p.ldc, p.M, p.N, p.K, 0, 0, 0};
+  i8_paths(p, es, &a);
   const size_t pc = (size_t)p.ldc * es, pr = (size_t)p.ldr * es;
-  a.c_word = bytes(p.C, pc);
-  a.r_word = p.residual ? bytes(p.residual, pr) : 0;
-  a.c_tma = a.c_word == 16;
-  a.r_tma = a.r_word == 16;
   CUtensorMap tmA, tmB, tmC, tmR;
   cudaError_t e = encode_tma_2d_ld(&tmA, 1, p.A, p.K, p.M, (size_t)p.lda, 128, 128);
   if (e != cudaSuccess) return e;
@@ -458,29 +494,443 @@ cudaError_t i8_launch(const Int8Gemm& p, int num_sms, cudaStream_t st) {
   if (a.c_tma) e = encode_tma_2d_ld(&tmC, es, p.C, p.N, p.M, pc, 128 / es, 32);
   if (e == cudaSuccess && a.r_tma) e = encode_tma_2d_ld(&tmR, es, p.residual, p.N, p.M, pr, 128 / es, 32);
   if (e != cudaSuccess) return e;
-  auto kern = int8_gemm_kernel<BN, kPair, T>;
+  const bool words = !a.c_tma || (p.residual && !a.r_tma);
+  auto kern = words ? int8_gemm_kernel<BN, kPair, true, T> : int8_gemm_kernel<BN, kPair, false, T>;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg::SMEM);
   if (e != cudaSuccess) return e;
   const long long tiles = (long long)((p.M + Cfg::TILE_M - 1) / Cfg::TILE_M) * ((p.N + BN - 1) / BN);
   const int units = kPair ? num_sms / 2 : num_sms;
   const int grid = tiles < units ? (int)tiles : units;
-  return kPair ? launch_pdl_pair(kern, dim3(2 * grid), dim3(Cfg::THREADS), Cfg::SMEM, st, tmA, tmB, tmC, tmR, a)
+  return kPair ? launch_pdl_cluster(kern, 2, dim3(2 * grid), dim3(Cfg::THREADS), Cfg::SMEM, st, tmA, tmB, tmC, tmR, a)
                : launch_pdl(kern, dim3(grid), dim3(Cfg::THREADS), Cfg::SMEM, st, tmA, tmB, tmC, tmR, a);
 }
 
+// ------------------------------------------------------------------ few rows
+// Up to 8 NT tokens: every weight is read once and used a few times, so what counts is
+// bytes in flight.  A CTA has 16 output channels, its 8 warps take 64-byte pieces of K in
+// turn and add up in shared memory at the end.  m16n8k32 products with the channels as
+// rows; a lane's 16 bytes of a row serve two of them (the sum over K may be taken in any
+// order as long as weights and tokens agree), so nothing passes through shared memory
+// on the way in.
+constexpr int kRowsWarps = 8;
+
+__device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                       uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+               : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// 16 codes of a weight row (used once: not kept in L1).
+__device__ __forceinline__ uint4 ld_once(const int8_t* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+
+// NT: groups of 8 tokens, CT: groups of 16 channels of a CTA; gridDim.y covers more tokens.
+template <int NT, int CT, class T>
+__global__ void __launch_bounds__(32 * kRowsWarps)
+    int8_gemm_rows_kernel(const int8_t* __restrict__ A, int lda, const int8_t* __restrict__ W, int ldw, const I8Args g) {
+  constexpr int U = NT + 2 * CT <= 4 ? 4 : NT + 2 * CT <= 6 ? 3 : 2;   // pieces of K in flight
+  constexpr int CH = 16 * CT;
+  __shared__ int part[kRowsWarps][NT * 8][CH + 1];
+  pdl_trigger();
+  pdl_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = lane >> 2, t = lane & 3;
+  const int n0 = blockIdx.x * CH, m0 = blockIdx.y * NT * 8;
+  // rows past the end repeat the last one; their sums are not used
+  const int8_t* w[2 * CT];
+  const int8_t* a[NT];
+#pragma unroll
+  for (int c = 0; c < 2 * CT; ++c) w[c] = W + (size_t)min(n0 + q + 8 * c, g.N - 1) * ldw + t * 16;
+#pragma unroll
+  for (int j = 0; j < NT; ++j) a[j] = A + (size_t)min(m0 + j * 8 + q, g.M - 1) * lda + t * 16;
+  int acc[CT][NT][4] = {};
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  for (int k = warp * 64; k < g.K; k += U * 64 * kRowsWarps) {
+    uint4 u[U][2 * CT], b[U][NT];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {   // codes past K lie within the padded rows (16-byte pitch)
+      const int kk = k + i * 64 * kRowsWarps;
+      const bool in = kk + t * 16 < g.K;
+#pragma unroll
+      for (int c = 0; c < 2 * CT; ++c) u[i][c] = in ? ld_once(w[c] + kk) : zero;
+#pragma unroll
+      for (int j = 0; j < NT; ++j) b[i][j] = in ? __ldg(reinterpret_cast<const uint4*>(a[j] + kk)) : zero;
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int left = g.K - (k + i * 64 * kRowsWarps + t * 16);   // codes of this piece inside K
+      if (left > 0 && left < 16) {   // the tokens' codes past K count as zero
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            const int keep = left - 4 * h;
+            uint32_t& v = (&b[i][j].x)[h];
+            v = keep >= 4 ? v : keep <= 0 ? 0u : v & ((1u << (8 * keep)) - 1u);
+          }
+      }
+#pragma unroll
+      for (int c = 0; c < CT; ++c)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          const uint4 &x = u[i][2 * c], &y = u[i][2 * c + 1];
+          mma_s8(acc[c][j], x.x, y.x, x.y, y.y, b[i][j].x, b[i][j].y);
+          mma_s8(acc[c][j], x.z, y.z, x.w, y.w, b[i][j].z, b[i][j].w);
+        }
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < CT; ++c)
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int h = 0; h < 4; ++h) part[warp][j * 8 + 2 * t + (h & 1)][c * 16 + q + 8 * (h >> 1)] = acc[c][j][h];
+  __syncthreads();
+  for (int e = threadIdx.x; e < NT * 8 * CH; e += 32 * kRowsWarps) {
+    const int m = m0 + e / CH, c = e % CH, n = n0 + c;
+    if (m >= g.M || n >= g.N) continue;
+    int sum = 0;
+#pragma unroll
+    for (int x = 0; x < kRowsWarps; ++x) sum += part[x][e / CH][c];
+    float v = __fmaf_rn(__fmul_rn(__int2float_rn(sum), __ldg(g.sA + m)), __ldg(g.sW + n),
+                        g.bias ? to_f32<T>(reinterpret_cast<const T*>(g.bias)[n]) : 0.f);
+    if (g.residual) v += to_f32<T>(reinterpret_cast<const T*>(g.residual)[(size_t)m * g.ldr + n]);
+    reinterpret_cast<T*>(g.C)[(size_t)m * g.ldc + n] = of_f32<T>(v);
+  }
+}
+
+// ------------------------------------------------------------------ split K
+// Few tiles: a cluster of S CTAs (2, 4 or 8) shares one 128 x BN tile, each with its part of
+// K.  CTA p finishes the BN / S columns p * BN / S ..; every CTA sorts its integer sums by
+// their owner in its own shared memory and sends each owner its block in one bulk copy, the
+// owner adds the S blocks (exact, so the order does not matter).  Read by the owner with
+// plain loads from the other CTAs' shared memory instead, the same sums took 4 to 6 us.
+// One tile per CTA, no persistence.  The ring is as deep as the part of K or shared memory
+// allows, so that narrow tiles keep as many bytes in flight as wide ones; A takes the rows
+// it has (M < 128), the MMA reads on into what follows, which only reaches sums of rows past
+// M.
+struct SplitCfg {
+  static constexpr int BM = 128, BK = 128, MAX_STAGES = 32;
+  static constexpr int THREADS = 384;                   // warps 0: TMA, 1: MMA, 4 .. 11: epilogue
+  static constexpr int BAR_BYTES = (2 * MAX_STAGES + 2) * 8 + 16;
+  static constexpr int COL_BYTES = 2 * 64 * 4;          // sW and bias of the CTA's columns
+  static constexpr int RING_BYTES = 144 * 1024;
+  static constexpr int IN_BYTES = 56 * 1024;            // blocks from the other CTAs: BN * 512 * (S - 1) / S
+  static constexpr size_t SMEM = (size_t)RING_BYTES + IN_BYTES + COL_BYTES + 1024 + BAR_BYTES;
+};
+static_assert(128 * 512 * 7 / 8 <= SplitCfg::IN_BYTES && 128 * 512 <= SplitCfg::RING_BYTES, "blocks");
+
+// The 8 epilogue warps of a split-K CTA.
+__device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+// 16-byte unit u of row r of a block of rows of `units` units (a power of two), placed so
+// that 8 rows' accesses to one unit meet all banks.
+__device__ __forceinline__ uint32_t block_at(int r, int u, int units) {
+  const int k = units < 8 ? units : 8;
+  return (uint32_t)(r * units + (u ^ ((r * k / 8) & (k - 1)))) * 16u;
+}
+
+template <int BN, class T>
+__global__ void __launch_bounds__(SplitCfg::THREADS, 1)
+    int8_gemm_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                           const I8Args g, int a_rows, int parts, int stages) {
+  using Cfg = SplitCfg;
+  constexpr int PER = 16 / (int)sizeof(T);
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  pdl_trigger();
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(base + Cfg::RING_BYTES + Cfg::IN_BYTES + Cfg::COL_BYTES);
+  uint8_t* in_s = base + Cfg::RING_BYTES;   // block of the k-th other CTA at k * block bytes
+  float* sw_s = reinterpret_cast<float*>(in_s + Cfg::IN_BYTES);
+  float* bias_s = sw_s + 64;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 2 * Cfg::MAX_STAGES + 2);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+  auto full = [&](int s) { return smem_u32(bars + s); };
+  auto empty = [&](int s) { return smem_u32(bars + Cfg::MAX_STAGES + s); };
+  const uint32_t done = smem_u32(bars + 2 * Cfg::MAX_STAGES), arrived = smem_u32(bars + 2 * Cfg::MAX_STAGES + 1);
+  const uint32_t stage_bytes = BN * Cfg::BK + (uint32_t)a_rows * Cfg::BK;   // A (whole 8-row units of 1 KB), then W
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)blockIdx.x % parts, tile = (int)blockIdx.x / parts;   // clusters are runs of `parts` blocks
+  const int tiles_m = (g.M + Cfg::BM - 1) / Cfg::BM;
+  const int m0 = tile % tiles_m * Cfg::BM, n0 = tile / tiles_m * BN;
+  const int nkb = (g.K + Cfg::BK - 1) / Cfg::BK;
+  const int kb0 = (int)((long long)nkb * rank / parts), kb1 = (int)((long long)nkb * (rank + 1) / parts);
+  if (threadIdx.x == 0) {
+    prefetch_tensormap(&tmA);
+    prefetch_tensormap(&tmB);
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), 1);
+    }
+    mbar_init(done, 1);
+    mbar_init(arrived, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    mbar_arrive_expect_tx(arrived, (uint32_t)(Cfg::BM * BN * 4 / parts) * (parts - 1));
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_holder), 128);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  cluster_sync_all();   // the other CTAs' barriers exist before anything signals them
+  tc_fence_after();
+  pdl_wait();   // inputs may be the previous kernel's outputs
+  const uint32_t tmem_base = *tmem_holder;
+  // this CTA's columns of the tile; an epilogue thread has one row of them and units of 8
+  // columns (half, half + 2, ...)
+  constexpr int UNITS = BN / 32;   // parts >= 2
+  const int cols = BN / parts, c_first = rank * cols;
+  const int quad = warp & 3, half = (warp >> 2) - 1, r = quad * 32 + lane, row = m0 + r;
+  const bool row_in = warp >= 4 && row < g.M;
+  const uint32_t block = Cfg::BM * BN * 4 / parts;   // bytes that go to one owner
+  bool sums_ok = false;
+  float sa = 0.f;
+  uint4 ru[UNITS][8 / PER];   // residual
+  if (warp == 0 && lane == 0) {
+    const uint32_t bytes = (uint32_t)(a_rows + BN) * Cfg::BK;
+    int stage = 0;
+    uint32_t phase = 0;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      if (!mbar_wait(empty(stage), phase ^ 1u, abort_flag)) break;
+      const uint32_t a = smem_u32(base) + stage * stage_bytes;
+      mbar_arrive_expect_tx(full(stage), bytes);
+      tma_load_2d(a + a_rows * Cfg::BK, &tmB, kb * Cfg::BK, n0, full(stage));
+      tma_load_2d(a, &tmA, kb * Cfg::BK, m0, full(stage));
+      if (++stage == stages) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    }
+  } else if (warp == 1 && lane == 0) {
+    constexpr uint32_t idesc = make_idesc_i8(128, BN);
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      if (!(ok = mbar_wait(full(stage), phase, abort_flag))) break;
+      tc_fence_after();
+      const uint32_t a = smem_u32(base) + stage * stage_bytes, b = a + a_rows * Cfg::BK;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (kb * Cfg::BK + 32 * k >= g.K) break;
+        mma_i8_ss(tmem_base, make_smem_desc(a + 32 * k, 16, 1024, kSwizzle128B),
+                  make_smem_desc(b + 32 * k, 16, 1024, kSwizzle128B), idesc, (kb > kb0 || k > 0) ? 1u : 0u);
+      }
+      tc_commit(empty(stage));
+      if (++stage == stages) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    }
+    if (ok) tc_commit(done);
+  } else if (warp >= 4) {   // this CTA's part, to its own shared memory (every load has been used)
+    // what the epilogue will need, on its way while the products run
+    if (threadIdx.x - 128 < cols) {
+      const int c = threadIdx.x - 128, n = n0 + c_first + c;
+      sw_s[c] = n < g.N ? __ldg(g.sW + n) : 0.f;
+      bias_s[c] = g.bias && n < g.N ? to_f32<T>(reinterpret_cast<const T*>(g.bias)[n]) : 0.f;
+    }
+    if (row_in) sa = __ldg(g.sA + row);
+#pragma unroll
+    for (int k = 0; k < UNITS; ++k) {
+      const int u = half + 2 * k, n = n0 + c_first + u * 8;
+#pragma unroll
+      for (int h = 0; h < 8 / PER; ++h) ru[k][h] = make_uint4(0u, 0u, 0u, 0u);
+      if (g.residual && row_in && u < cols / 8 && n < g.N) {
+        const T* res = reinterpret_cast<const T*>(g.residual) + (size_t)row * g.ldr + n;
+        if (n + 8 <= g.N && g.r_tma) {
+#pragma unroll
+          for (int h = 0; h < 8 / PER; ++h) ru[k][h] = reinterpret_cast<const uint4*>(res)[h];
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (n + i < g.N) reinterpret_cast<T*>(&ru[k][0])[i] = res[i];
+        }
+      }
+    }
+    const bool ok = mbar_wait(done, 0, abort_flag);
+    if (__all_sync(0xffffffffu, ok) && m0 + quad * 32 < g.M) {
+      tc_fence_after();
+#pragma unroll
+      for (int gr = 0; gr < (BN + 63) / 64; ++gr) {
+        const int c = half * (BN / 2) + gr * 32;
+        if (BN < 64 && half) break;
+        uint32_t v[32];
+        tmem_ld32(tmem_base + ((uint32_t)(quad * 32) << 16) + c, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int owner = (c + 4 * i) / cols, u = (c + 4 * i - owner * cols) / 4;
+          *reinterpret_cast<uint4*>(base + owner * block + block_at(r, u, cols / 4)) =
+              make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        }
+      }
+      tc_fence_before();
+    }
+    fence_proxy_async_smem();
+    epilogue_sync();   // reached by all 8 warps, after a timed-out wait too
+    if (threadIdx.x == 128) {   // rows past M are sent as they are: nobody reads them
+      for (int k = 1; k < parts; ++k) {
+        const int to = (rank + k) % parts, slot = parts - 1 - k;   // this CTA is `to`'s (parts - k)-th neighbour
+        bulk_copy_cluster(mapa_shared(smem_u32(in_s) + slot * block, to), smem_u32(base) + to * block, block,
+                          mapa_shared(arrived, to));
+      }
+    }
+    sums_ok = mbar_wait(arrived, 0, abort_flag) && ok;
+    sums_ok = __all_sync(0xffffffffu, sums_ok);
+  }
+  if (row_in && sums_ok) {
+#pragma unroll
+    for (int k = 0; k < UNITS; ++k) {
+      const int u = half + 2 * k, c = c_first + u * 8, n = n0 + c;
+      if (u < cols / 8 && n < g.N) {
+        int4 lo = make_int4(0, 0, 0, 0), hi = lo;
+#pragma unroll 4
+        for (int p = 0; p < parts; ++p) {
+          const uint8_t* src = p == 0 ? base + rank * block : in_s + (p - 1) * block;
+          const int4 a = *reinterpret_cast<const int4*>(src + block_at(r, 2 * u, cols / 4));
+          const int4 b = *reinterpret_cast<const int4*>(src + block_at(r, 2 * u + 1, cols / 4));
+          lo = make_int4(lo.x + a.x, lo.y + a.y, lo.z + a.z, lo.w + a.w);
+          hi = make_int4(hi.x + b.x, hi.y + b.y, hi.z + b.z, hi.w + b.w);
+        }
+        const int acc[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+        float v[8];
+#pragma unroll
+        for (int h = 0; h < 8 / PER; ++h) unpack16<T>(ru[k][h], v + h * PER);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          v[i] += __fmaf_rn(__fmul_rn(__int2float_rn(acc[i]), sa), sw_s[u * 8 + i], bias_s[u * 8 + i]);
+        T* out = reinterpret_cast<T*>(g.C) + (size_t)row * g.ldc + n;
+        if (n + 8 <= g.N && g.c_tma) {
+#pragma unroll
+          for (int h = 0; h < 8 / PER; ++h) reinterpret_cast<uint4*>(out)[h] = pack16<T>(v + h * PER);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (n + i < g.N) out[i] = of_f32<T>(v[i]);
+        }
+      }
+    }
+  }
+  __syncthreads();
+  if (*abort_flag) settle_pause(50000);
+  cluster_sync_all();   // no CTA leaves before every copy between them has arrived
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem_base, 128);
+  }
+}
+
+template <int BN, class T>
+cudaError_t i8_launch_split(const Int8Gemm& p, int parts, cudaStream_t st) {
+  using Cfg = SplitCfg;
+  I8Args a{p.sA, p.sW, p.bias, p.residual, p.C, p.ldr, p.ldc, p.M, p.N, p.K, 0, 0, 0};
+  i8_paths(p, (int)sizeof(T), &a);
+  const int a_rows = p.M < Cfg::BM ? (p.M + 7) / 8 * 8 : Cfg::BM;
+  const int stage_bytes = (BN + a_rows) * Cfg::BK;
+  const int nkb = ((p.K + 127) / 128 + parts - 1) / parts;
+  // the MMA of the last stage reads 16 KB from the start of its A tile on
+  const int behind = stage_bytes < Cfg::BM * Cfg::BK ? Cfg::BM * Cfg::BK - stage_bytes : 0;
+  int stages = (Cfg::RING_BYTES - behind) / stage_bytes;
+  if (stages > Cfg::MAX_STAGES) stages = Cfg::MAX_STAGES;
+  if (stages > nkb) stages = nkb;
+  CUtensorMap tmA, tmB;
+  cudaError_t e = encode_tma_2d_ld(&tmA, 1, p.A, p.K, p.M, (size_t)p.lda, 128, a_rows);
+  if (e != cudaSuccess) return e;
+  e = encode_tma_2d_ld(&tmB, 1, p.W, p.K, p.N, (size_t)p.ldw, 128, BN);
+  if (e != cudaSuccess) return e;
+  auto kern = int8_gemm_split_kernel<BN, T>;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg::SMEM);
+  if (e != cudaSuccess) return e;
+  const int tiles = ((p.M + Cfg::BM - 1) / Cfg::BM) * ((p.N + BN - 1) / BN);
+  return launch_pdl_cluster(kern, parts, dim3(tiles * parts), dim3(Cfg::THREADS), Cfg::SMEM, st, tmA, tmB, a, a_rows,
+                            parts, stages);
+}
+
+template <int NT, int CT, class T>
+cudaError_t i8_launch_rows(const Int8Gemm& p, cudaStream_t st) {
+  const I8Args a{p.sA, p.sW, p.bias, p.residual, p.C, p.ldr, p.ldc, p.M, p.N, p.K, 0, 0, 0};
+  return launch_pdl(int8_gemm_rows_kernel<NT, CT, T>, dim3((p.N + 16 * CT - 1) / (16 * CT), (p.M + 8 * NT - 1) / (8 * NT)),
+                    dim3(32 * kRowsWarps), 0, st, p.A, p.lda, p.W, p.ldw, a);
+}
+
+// Which kernel: the least of these estimates, in microseconds, fitted to back-to-back calls
+// on B200 (148 SMs) over 1 <= M <= 25024, 300 <= N <= 4608, 512 <= K <= 4608; nkb = K / 128.
+//  * a 128-column K block of a 128 x 64 or 128 x 128 tile takes 0.33 us whatever its width
+//    (4 MMAs of about 150 cycles; 0.40 us once the GPU is full), of a 256 x 256 pair 0.42;
+//  * the fixed part is 3.7 us for single tiles, 5.2 for pairs, 5.4 to 6.6 for clusters (which
+//    fit the GPU 74, 33 and 15 at a time for 2, 4 and 8 CTAs);
+//  * few rows: 2 us and what passes through L2, weights once per group of tokens and tokens
+//    once per group of channels, at 7.4 TB/s.
+// Measured, the kernel chosen against the next best: 1 x 4608 x 4608 6.0 us (few rows)
+// against 11.7; 48 x 4608 x 1152 6.2 (tile) against 6.2 (few rows); 128 x 1152 x 4304 8.1 (64
+// wide, 4 parts) against 8.3; 243 x 2048 x 4608 10.3 (128 wide, 4 parts) against 11.6;
+// 972 x 1152 x 1152 6.8 (tile) against 8.1 (pairs); 6256 x 1152 x 1152 12.8 (pairs) against 14.8.
+enum I8Kernel { kRows11, kRows21, kRows22, kRows41, kTile, kPairs, kSplit64x2, kSplit64x4, kSplit128x2, kSplit128x4, kSplit128x8 };
+
+I8Kernel i8_choose(int M, int N, int K, int num_sms) {
+  if (M <= 8) return kRows11;
+  const double nkb = (K + 127) / 128, nk = (double)N * K;
+  auto tiles = [&](int bm, int bn) { return (double)((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
+  I8Kernel best = kTile;
+  double least = 1e30;
+  auto offer = [&](I8Kernel k, double us) {
+    if (us < least) {
+      least = us;
+      best = k;
+    }
+  };
+  const double waves = std::ceil(tiles(128, 128) / num_sms);
+  offer(kTile, 3.7 + nkb * (waves == 1 ? 0.33 : 0.40 * waves));
+  offer(kPairs, 5.2 + nkb * 0.42 * std::ceil(tiles(256, 256) / (num_sms / 2)));
+  auto split = [&](I8Kernel k, int bn, int parts, int fit, double fixed) {
+    if (M <= 1024 && nkb >= parts && tiles(128, bn) <= fit) offer(k, fixed + 0.33 * std::ceil(nkb / parts));
+  };
+  split(kSplit64x2, 64, 2, num_sms / 2, 5.4);
+  split(kSplit64x4, 64, 4, 33, 5.6);
+  split(kSplit128x2, 128, 2, num_sms / 2, 6.6);
+  split(kSplit128x4, 128, 4, 33, 6.6);
+  split(kSplit128x8, 128, 8, 15, 6.3);
+  auto rows = [&](I8Kernel k, int tokens, int channels) {
+    offer(k, 2.0 + 1.35e-7 * (nk * ((M + tokens - 1) / tokens) + nk / channels * M));
+  };
+  if (M > 64) rows(kRows41, 32, 16);
+  else if (M > 16 && N >= 32 * 128) rows(kRows22, 16, 32);
+  else rows(kRows21, 16, 16);
+  return best;
+}
+
 template <class T>
-cudaError_t i8_pick(const Int8Gemm& p, int num_sms, cudaStream_t st) {
-  if (p.M > 1024 && p.N > 128) return i8_launch<256, true, T>(p, num_sms, st);
-  return p.N > 128 ? i8_launch<256, false, T>(p, num_sms, st) : i8_launch<128, false, T>(p, num_sms, st);
+cudaError_t i8_run(const Int8Gemm& p, int num_sms, cudaStream_t st) {
+  switch (i8_choose(p.M, p.N, p.K, num_sms)) {
+    case kRows11: return i8_launch_rows<1, 1, T>(p, st);
+    case kRows21: return i8_launch_rows<2, 1, T>(p, st);
+    case kRows22: return i8_launch_rows<2, 2, T>(p, st);
+    case kRows41: return i8_launch_rows<4, 1, T>(p, st);
+    case kTile: return i8_launch<128, false, T>(p, num_sms, st);
+    case kPairs: return i8_launch<256, true, T>(p, num_sms, st);
+    case kSplit64x2: return i8_launch_split<64, T>(p, 2, st);
+    case kSplit64x4: return i8_launch_split<64, T>(p, 4, st);
+    case kSplit128x2: return i8_launch_split<128, T>(p, 2, st);
+    case kSplit128x4: return i8_launch_split<128, T>(p, 4, st);
+    case kSplit128x8: return i8_launch_split<128, T>(p, 8, st);
+  }
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace
 
 cudaError_t launch_int8_gemm(const Int8Gemm& p, int num_sms, cudaStream_t st) {
   if (p.M == 0) return cudaSuccess;
-  if (p.dtype == 0) return i8_pick<__nv_bfloat16>(p, num_sms, st);
-  if (p.dtype == 1) return i8_pick<__half>(p, num_sms, st);
-  return i8_pick<float>(p, num_sms, st);
+  if (p.dtype == 0) return i8_run<__nv_bfloat16>(p, num_sms, st);
+  if (p.dtype == 1) return i8_run<__half>(p, num_sms, st);
+  return i8_run<float>(p, num_sms, st);
 }
 
 }  // namespace vitq
