@@ -46,47 +46,54 @@ __device__ __forceinline__ void unpack16(const uint4& u, float* v) {
 #pragma unroll
   for (int i = 0; i < (int)(16 / sizeof(T)); ++i) v[i] = to_f32<T>(p[i]);
 }
-template <class T>
-__device__ __forceinline__ uint4 pack16(const float* v) {
+template <class T> __device__ __forceinline__ uint4 pack16(const float* v);
+template <> __device__ __forceinline__ uint4 pack16<float>(const float* v) {
+  return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+}
+template <> __device__ __forceinline__ uint4 pack16<__nv_bfloat16>(const float* v) {
+  return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+}
+template <> __device__ __forceinline__ uint4 pack16<__half>(const float* v) {
   uint4 u;
-  T* p = reinterpret_cast<T*>(&u);
 #pragma unroll
-  for (int i = 0; i < (int)(16 / sizeof(T)); ++i) p[i] = of_f32<T>(v[i]);
+  for (int i = 0; i < 4; ++i) {
+    const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+    (&u.x)[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
   return u;
 }
 
 // ------------------------------------------------------------------ tiles
 // kPair: two CTAs (cta_group::2) share one 256 x BN tile: each holds 128 rows of A, half
 // of the W rows, and the accumulator of its own 128 rows.
-template <int BN, bool kPair>
+template <int BN, bool kPair, int kCols>
 struct I8Cfg {
   static constexpr int BM = 128, BK = 128;   // 128 codes = one 128B swizzle row
   static constexpr int TILE_M = kPair ? 256 : 128;
   static constexpr int B_ROWS = kPair ? BN / 2 : BN;
-  static constexpr int STAGES = 4;
+  static constexpr int STAGES = BN / kCols > 2 ? 4 : 5;
   static constexpr int A_BYTES = BM * BK;
   static constexpr int B_BYTES = B_ROWS * BK;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
   static constexpr int NACC = 2;              // TMEM accumulators, alternating between tiles
-  static constexpr int EPI_WARPS = 8, EPI_WARP0 = 4;   // a row quadrant and half of the columns each
-  static constexpr int COLS = BN / 2;                  // columns of an epilogue warp
+  static constexpr int COLS = kCols;                   // columns of an epilogue warp (and a row quadrant)
+  static constexpr int EPI_WARPS = BN / COLS * 4, EPI_WARP0 = 4;
   static constexpr int THREADS = 32 * (EPI_WARP0 + EPI_WARPS);
   static constexpr int BOX_BYTES = 4096;      // 32 rows x 128 bytes of C
-  static constexpr int BOXES = 2;             // per epilogue warp
-  static constexpr int OUT_BYTES = EPI_WARPS * BOXES * BOX_BYTES;
+  static constexpr int OUT_BYTES = EPI_WARPS * BOX_BYTES;
   static constexpr int COL_BYTES = EPI_WARPS * COLS * 8;   // sW, then bias, of the warp's columns
-  static constexpr int BAR_BYTES = (2 * STAGES + 2 * NACC + EPI_WARPS * BOXES) * 8 + 16;
+  static constexpr int BAR_BYTES = (2 * STAGES + 2 * NACC + EPI_WARPS) * 8 + 16;
   static constexpr size_t SMEM = (size_t)STAGES * STAGE_BYTES + OUT_BYTES + COL_BYTES + 1024 + BAR_BYTES;
 };
 
-template <int BN, bool kPair>
+template <class Config>
 struct I8Smem {
-  using Cfg = I8Cfg<BN, kPair>;
+  using Cfg = Config;
   uint8_t* base;
   __device__ uint32_t a(int s) const { return smem_u32(base + (size_t)s * Cfg::STAGE_BYTES); }
   __device__ uint32_t b(int s) const { return a(s) + Cfg::A_BYTES; }
   __device__ uint8_t* out(int w) const {
-    return base + (size_t)Cfg::STAGES * Cfg::STAGE_BYTES + (size_t)w * Cfg::BOXES * Cfg::BOX_BYTES;
+    return base + (size_t)Cfg::STAGES * Cfg::STAGE_BYTES + (size_t)w * Cfg::BOX_BYTES;
   }
   __device__ float* cols(int w) const {
     return reinterpret_cast<float*>(base + (size_t)Cfg::STAGES * Cfg::STAGE_BYTES + Cfg::OUT_BYTES) + w * 2 * Cfg::COLS;
@@ -98,26 +105,26 @@ struct I8Smem {
   __device__ uint32_t empty(int s) const { return smem_u32(bars() + Cfg::STAGES + s); }
   __device__ uint32_t tfull(int b) const { return smem_u32(bars() + 2 * Cfg::STAGES + b); }
   __device__ uint32_t tempty(int b) const { return smem_u32(bars() + 2 * Cfg::STAGES + Cfg::NACC + b); }
-  __device__ uint32_t res_full(int w, int slot) const {
-    return smem_u32(bars() + 2 * Cfg::STAGES + 2 * Cfg::NACC + w * Cfg::BOXES + slot);
-  }
+  __device__ uint32_t res_full(int w) const { return smem_u32(bars() + 2 * Cfg::STAGES + 2 * Cfg::NACC + w); }
   __device__ uint32_t* tmem_holder() const {
-    return reinterpret_cast<uint32_t*>(bars() + 2 * Cfg::STAGES + 2 * Cfg::NACC + Cfg::EPI_WARPS * Cfg::BOXES);
+    return reinterpret_cast<uint32_t*>(bars() + 2 * Cfg::STAGES + 2 * Cfg::NACC + Cfg::EPI_WARPS);
   }
   __device__ volatile int* abort_flag() const { return reinterpret_cast<volatile int*>(tmem_holder() + 1); }
 };
 
-// Tile order of the other GEMMs: CTAs that run together read different W tiles.
+// Tile order: down 8 row tiles, then to the next column tile, so that CTAs that run
+// together share tiles of both operands (25024 x 3456 x 1152: 101.5 us, against 105.1 in
+// the diagonal order of the other GEMMs).
 __device__ __forceinline__ void i8_tile_coords(int tile, int tiles_m, int tiles_n, int& m, int& n) {
-  m = tile % tiles_m;
-  n = (tile / tiles_m + m) % tiles_n;
+  const int group = tile / (8 * tiles_n), in = tile - group * 8 * tiles_n, rows = min(8, tiles_m - 8 * group);
+  n = in / rows;
+  m = 8 * group + in - n * rows;
 }
 
 // Tiles of this CTA (or pair): t0, t0 + dt, ...
-template <int BN, bool kPair>
-__device__ void i8_producer(const I8Smem<BN, kPair>& sm, const CUtensorMap* tmA, const CUtensorMap* tmB, int tiles_m,
+template <int BN, bool kPair, class Cfg>
+__device__ void i8_producer(const I8Smem<Cfg>& sm, const CUtensorMap* tmA, const CUtensorMap* tmB, int tiles_m,
                             int tiles_n, int num_tiles, int nkb, int t0, int dt, int rank) {
-  using Cfg = I8Cfg<BN, kPair>;
   int stage = 0;
   uint32_t phase = 0;
   for (int tile = t0; tile < num_tiles; tile += dt) {
@@ -144,9 +151,8 @@ __device__ void i8_producer(const I8Smem<BN, kPair>& sm, const CUtensorMap* tmA,
   }
 }
 
-template <int BN, bool kPair>
-__device__ void i8_mma(const I8Smem<BN, kPair>& sm, uint32_t tmem_base, int num_tiles, int nkb, int K, int t0, int dt) {
-  using Cfg = I8Cfg<BN, kPair>;
+template <int BN, bool kPair, class Cfg>
+__device__ void i8_mma(const I8Smem<Cfg>& sm, uint32_t tmem_base, int num_tiles, int nkb, int K, int t0, int dt) {
   constexpr uint32_t idesc = make_idesc_i8(Cfg::TILE_M, BN);
   int stage = 0;
   uint32_t phase = 0, it = 0;
@@ -236,52 +242,49 @@ __device__ __noinline__ void box_store(const uint8_t* slot, uint8_t* mat, size_t
   }
 }
 
-// Epilogue warp: 32 rows (thread = row) and COLS columns, 32 columns at a time; the next
-// 32 columns' accumulators are on their way while the present ones are scaled.  Each
-// 128-byte-wide box of C has one of two slots in shared memory: the residual is brought
-// there first (for the first two boxes of a tile while its sum is still running), the
-// finished box leaves from there.
+// Epilogue warp: 32 rows (thread = row) and 64 columns, 32 columns at a time; four warps a
+// scheduler (256 columns) hide each other's latencies.  A 128-byte-wide box of C (one, or
+// two in fp32) has a slot in shared memory: the residual is brought there first (for the
+// first box while the tile's sum is still running), the finished box leaves from there.
 // kWords: C or the residual may need word-by-word rows (a kernel of its own: the extra
 // paths spill registers, 6 % of a large product's time).
-template <int BN, bool kPair, bool kWords, class T>
-__device__ void i8_epilogue(const I8Smem<BN, kPair>& sm, uint32_t tmem_base, const I8Args& g, const CUtensorMap* tmC,
+template <int BN, bool kPair, bool kWords, class T, class Cfg>
+__device__ void i8_epilogue(const I8Smem<Cfg>& sm, uint32_t tmem_base, const I8Args& g, const CUtensorMap* tmC,
                             const CUtensorMap* tmR, int tiles_m, int tiles_n, int num_tiles, int t0, int dt, int rank) {
-  using Cfg = I8Cfg<BN, kPair>;
   constexpr int PER = 16 / (int)sizeof(T);          // elements per 16 bytes
   constexpr int BOXC = 128 / (int)sizeof(T);        // columns per box
-  constexpr int GROUPS = Cfg::COLS / 32, PER_BOX = BOXC / 32, NBOX = Cfg::COLS / BOXC;
+  constexpr int PER_BOX = BOXC / 32, NBOX = Cfg::COLS / BOXC;
   // the leader's tempty barriers count both CTAs' epilogue warps
   const uint32_t tempty0 = kPair ? mapa_shared(sm.tempty(0), 0) : sm.tempty(0);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int ew = warp - Cfg::EPI_WARP0, quad = warp & 3, half = ew >> 2;
-  uint8_t* stg = sm.out(ew);
+  const int ew = warp - Cfg::EPI_WARP0, quad = warp & 3, part = ew >> 2;
+  uint8_t* slot = sm.out(ew);
   float* sw_s = sm.cols(ew);
   float* bias_s = sw_s + Cfg::COLS;
   const T* bias = reinterpret_cast<const T*>(g.bias);
   const bool has_res = g.residual != nullptr;
-  uint32_t it = 0, slot_it = 0, res_phase = 0;   // boxes so far; phase of each slot's residual barrier
+  uint32_t it = 0, res_phase = 0;
   for (int tile = t0; tile < num_tiles; tile += dt, ++it) {
     int mt, nt;
     i8_tile_coords(tile, tiles_m, tiles_n, mt, nt);
-    const int col0 = nt * BN + half * Cfg::COLS;
+    const int col0 = nt * BN + part * Cfg::COLS;
     const int y0 = mt * Cfg::TILE_M + rank * Cfg::BM + quad * 32, row = y0 + lane;
     const uint32_t acc = it % Cfg::NACC;
-    const int groups = y0 < g.M ? min(GROUPS, (g.N - col0 + 31) >> 5) : 0;   // groups inside C (may be < 0)
-    const int nbox = (groups + PER_BOX - 1) / PER_BOX;
+    const int nbox = y0 < g.M ? min(NBOX, (g.N - col0 + BOXC - 1) / BOXC) : 0;   // boxes with a column of C (may be < 0)
     const int rows = min(32, g.M - y0);
-    // brings the residual of box b of this tile to its slot, once the slot's last store has read it
+    // brings the residual of box b of this tile to the slot, once the last store has read it
     auto fetch_res = [&](int b) {
-      uint8_t* slot = stg + ((slot_it + b) & 1u) * Cfg::BOX_BYTES;
       const int c0 = col0 + b * BOXC;
+      if (lane == 0) bulk_wait_read_all();
       if (!kWords || g.r_tma) {
         fence_proxy_async_smem();   // the warp's own accesses to the slot come before the copy
         __syncwarp();
         if (lane == 0) {
-          const uint32_t bar = sm.res_full(ew, (slot_it + b) & 1u);
-          mbar_arrive_expect_tx(bar, Cfg::BOX_BYTES);
-          tma_load_2d(smem_u32(slot), tmR, c0, y0, bar);
+          mbar_arrive_expect_tx(sm.res_full(ew), Cfg::BOX_BYTES);
+          tma_load_2d(smem_u32(slot), tmR, c0, y0, sm.res_full(ew));
         }
       } else {
+        __syncwarp();
         const uint8_t* mat = reinterpret_cast<const uint8_t*>(g.residual) + ((size_t)y0 * g.ldr + c0) * sizeof(T);
         const int bytes = min(128, (g.N - c0) * (int)sizeof(T));
         if (g.r_word == 4) box_load<uint32_t>(slot, mat, (size_t)g.ldr * sizeof(T), rows, bytes);
@@ -289,12 +292,7 @@ __device__ void i8_epilogue(const I8Smem<BN, kPair>& sm, uint32_t tmem_base, con
         __syncwarp();
       }
     };
-    if (has_res && nbox > 0) {
-      if (lane == 0) bulk_wait_read_all();
-      __syncwarp();
-      fetch_res(0);
-      if (nbox > 1) fetch_res(1);
-    }
+    if (has_res && nbox > 0) fetch_res(0);
     __syncwarp();
 #pragma unroll
     for (int c = lane; c < Cfg::COLS; c += 32) {
@@ -308,59 +306,53 @@ __device__ void i8_epilogue(const I8Smem<BN, kPair>& sm, uint32_t tmem_base, con
     bool ok = mbar_wait(sm.tfull(acc), (it / Cfg::NACC) & 1u, sm.abort_flag());
     if (!__all_sync(0xffffffffu, ok)) return;
     tc_fence_after();
-    const uint32_t taddr = tmem_base + ((uint32_t)(quad * 32) << 16) + acc * BN + half * Cfg::COLS;
-    uint32_t r[2][32];
-    if (groups > 0) tmem_ld32(taddr, r[0]);
+    const uint32_t taddr = tmem_base + ((uint32_t)(quad * 32) << 16) + acc * BN + part * Cfg::COLS;
 #pragma unroll
     for (int b = 0; b < NBOX; ++b) {
       if (b < nbox) {   // uniform
-        const uint32_t s = (slot_it + b) & 1u;
-        uint8_t* slot = stg + s * Cfg::BOX_BYTES;
         if (has_res) {
+          if (b > 0) fetch_res(b);
           if (!kWords || g.r_tma) {
-            ok = mbar_wait(sm.res_full(ew, s), (res_phase >> s) & 1u, sm.abort_flag());
+            ok = mbar_wait(sm.res_full(ew), res_phase, sm.abort_flag());
             if (!__all_sync(0xffffffffu, ok)) return;
-            res_phase ^= 1u << s;
+            res_phase ^= 1u;
           }
-        } else if (!kWords || g.c_tma) {   // the store before last has read its box
-          if (lane == 0) bulk_wait_read<1>();
+        } else if (!kWords || g.c_tma) {   // the last store has read the slot
+          if (lane == 0) bulk_wait_read_all();
           __syncwarp();
         }
 #pragma unroll
         for (int h = 0; h < PER_BOX; ++h) {
-          const int gr = b * PER_BOX + h;
-          if (gr < groups) {
-            tmem_wait_ld();
-            if (gr + 1 < groups) tmem_ld32(taddr + (gr + 1) * 32, r[(gr + 1) & 1]);
+          const int gr = b * PER_BOX + h;   // 32 columns (past N: zero scales)
+          uint32_t r[32];
+          tmem_ld32(taddr + gr * 32, r);
+          tmem_wait_ld();
 #pragma unroll
-            for (int c = 0; c < 32 / PER; ++c) {
-              float v[PER];
+          for (int c = 0; c < 32 / PER; ++c) {
+            float v[PER];
 #pragma unroll
-              for (int i = 0; i < PER; i += 4) {
-                const int at = gr * 32 + c * PER + i;
-                const float4 w = *reinterpret_cast<const float4*>(sw_s + at);
-                const float4 bi = *reinterpret_cast<const float4*>(bias_s + at);
-                const uint32_t* a = r[gr & 1] + c * PER + i;
-                const float2 lo =
-                    f2unpack(ffma2(fmul2(f2pack(__int2float_rn((int)a[0]), __int2float_rn((int)a[1])), sa2),
-                                   f2pack(w.x, w.y), f2pack(bi.x, bi.y)));
-                const float2 hi =
-                    f2unpack(ffma2(fmul2(f2pack(__int2float_rn((int)a[2]), __int2float_rn((int)a[3])), sa2),
-                                   f2pack(w.z, w.w), f2pack(bi.z, bi.w)));
-                v[i] = lo.x;
-                v[i + 1] = lo.y;
-                v[i + 2] = hi.x;
-                v[i + 3] = hi.y;
-              }
-              uint4* at = reinterpret_cast<uint4*>(slot + box_at(lane, h * 32 * (int)sizeof(T) + c * 16));
-              if (has_res) {
-                float rv[PER];
-                unpack16<T>(*at, rv);
-#pragma unroll
-                for (int i = 0; i < PER; ++i) v[i] += rv[i];
-              }
-              *at = pack16<T>(v);
+            for (int i = 0; i < PER; i += 4) {
+              const int at = gr * 32 + c * PER + i;
+              const float4 w = *reinterpret_cast<const float4*>(sw_s + at);
+              const float4 bi = *reinterpret_cast<const float4*>(bias_s + at);
+              const uint32_t* a = r + c * PER + i;
+              const float2 lo = f2unpack(ffma2(fmul2(f2pack(__int2float_rn((int)a[0]), __int2float_rn((int)a[1])), sa2),
+                                               f2pack(w.x, w.y), f2pack(bi.x, bi.y)));
+              const float2 hi = f2unpack(ffma2(fmul2(f2pack(__int2float_rn((int)a[2]), __int2float_rn((int)a[3])), sa2),
+                                               f2pack(w.z, w.w), f2pack(bi.z, bi.w)));
+              v[i] = lo.x;
+              v[i + 1] = lo.y;
+              v[i + 2] = hi.x;
+              v[i + 3] = hi.y;
             }
+            uint4* at = reinterpret_cast<uint4*>(slot + box_at(lane, h * 32 * (int)sizeof(T) + c * 16));
+            if (has_res) {
+              float rv[PER];
+              unpack16<T>(*at, rv);
+#pragma unroll
+              for (int i = 0; i < PER; ++i) v[i] += rv[i];
+            }
+            *at = pack16<T>(v);
           }
         }
         const int c0 = col0 + b * BOXC;
@@ -370,7 +362,6 @@ __device__ void i8_epilogue(const I8Smem<BN, kPair>& sm, uint32_t tmem_base, con
           if (lane == 0) {   // TMA clips rows past M and columns past N
             tma_store_2d(tmC, smem_u32(slot), c0, y0);
             bulk_commit_group();
-            if (has_res && b + 2 < nbox) bulk_wait_read<0>();
           }
         } else {
           __syncwarp();
@@ -379,10 +370,8 @@ __device__ void i8_epilogue(const I8Smem<BN, kPair>& sm, uint32_t tmem_base, con
           box_store<std::conditional_t<sizeof(T) == 2, uint16_t, uint32_t>>(slot, mat, (size_t)g.ldc * sizeof(T), rows, bytes);
         }
         __syncwarp();
-        if (has_res && b + 2 < nbox) fetch_res(b + 2);
       }
     }
-    if (nbox > 0) slot_it += nbox;
     tc_fence_before();
     __syncwarp();
     if (lane == 0) {
@@ -395,15 +384,15 @@ __device__ void i8_epilogue(const I8Smem<BN, kPair>& sm, uint32_t tmem_base, con
   if (lane == 0) bulk_wait_all();
 }
 
-template <int BN, bool kPair, bool kWords, class T>
-__global__ void __launch_bounds__(I8Cfg<BN, kPair>::THREADS, 1)
+template <int BN, bool kPair, int kCols, bool kWords, class T>
+__global__ void __launch_bounds__(I8Cfg<BN, kPair, kCols>::THREADS, 1)
     int8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                      const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmR,
                      const I8Args args) {
-  using Cfg = I8Cfg<BN, kPair>;
+  using Cfg = I8Cfg<BN, kPair, kCols>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   pdl_trigger();
-  I8Smem<BN, kPair> sm;
+  I8Smem<Cfg> sm;
   sm.base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int nkb = (args.K + Cfg::BK - 1) / Cfg::BK;
@@ -422,8 +411,7 @@ __global__ void __launch_bounds__(I8Cfg<BN, kPair>::THREADS, 1)
       mbar_init(sm.tfull(b), 1);
       mbar_init(sm.tempty(b), Cfg::EPI_WARPS * (kPair ? 2 : 1));
     }
-    for (int w = 0; w < Cfg::EPI_WARPS; ++w)
-      for (int b = 0; b < Cfg::BOXES; ++b) mbar_init(sm.res_full(w, b), 1);
+    for (int w = 0; w < Cfg::EPI_WARPS; ++w) mbar_init(sm.res_full(w), 1);
     *sm.abort_flag() = 0;
     fence_barrier_init();
   }
@@ -478,9 +466,9 @@ void i8_paths(const Int8Gemm& p, int es, I8Args* a) {
   a->r_tma = a->r_word == 16;
 }
 
-template <int BN, bool kPair, class T>
-cudaError_t i8_launch(const Int8Gemm& p, int num_sms, cudaStream_t st) {
-  using Cfg = I8Cfg<BN, kPair>;
+template <int BN, bool kPair, int kCols, class T>
+cudaError_t i8_launch(const Int8Gemm& p, bool words, int num_sms, cudaStream_t st) {
+  using Cfg = I8Cfg<BN, kPair, kCols>;
   constexpr int es = (int)sizeof(T);
   I8Args a{p.sA, p.sW, p.bias, p.residual, p.C, p.ldr, p.ldc, p.M, p.N, p.K, 0, 0, 0};
   i8_paths(p, es, &a);
@@ -494,8 +482,10 @@ cudaError_t i8_launch(const Int8Gemm& p, int num_sms, cudaStream_t st) {
   if (a.c_tma) e = encode_tma_2d_ld(&tmC, es, p.C, p.N, p.M, pc, 128 / es, 32);
   if (e == cudaSuccess && a.r_tma) e = encode_tma_2d_ld(&tmR, es, p.residual, p.N, p.M, pr, 128 / es, 32);
   if (e != cudaSuccess) return e;
-  const bool words = !a.c_tma || (p.residual && !a.r_tma);
-  auto kern = words ? int8_gemm_kernel<BN, kPair, true, T> : int8_gemm_kernel<BN, kPair, false, T>;
+  constexpr bool kMayWords = kCols == 64;   // see i8_pairs
+  auto kern = int8_gemm_kernel<BN, kPair, kCols, false, T>;
+  if constexpr (kMayWords)
+    if (words) kern = int8_gemm_kernel<BN, kPair, kCols, true, T>;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg::SMEM);
   if (e != cudaSuccess) return e;
   const long long tiles = (long long)((p.M + Cfg::TILE_M - 1) / Cfg::TILE_M) * ((p.N + BN - 1) / BN);
@@ -860,6 +850,22 @@ cudaError_t i8_launch_rows(const Int8Gemm& p, cudaStream_t st) {
                     dim3(32 * kRowsWarps), 0, st, p.A, p.lda, p.W, p.ldw, a);
 }
 
+// Pairs' epilogue: 8 warps (128 columns each) and 5 stages while the sums take longer than
+// it, else 16 warps (64 columns) and 4. 25024 x 3456 x 1152: 101.5 against 109.4 us;
+// 20000 x 2688 x 221: 38.1 against 32.9 us. Rows moved word by word: always 16 warps.
+template <class T>
+cudaError_t i8_pairs(const Int8Gemm& p, bool words, int num_sms, cudaStream_t st) {
+  return words || p.K <= 512 ? i8_launch<256, true, 64, T>(p, words, num_sms, st)
+                             : i8_launch<256, true, 128, T>(p, false, num_sms, st);
+}
+
+// Whether C or the residual has rows that TMA cannot address.
+bool i8_words(const Int8Gemm& p) {
+  I8Args a{};
+  i8_paths(p, p.dtype == 2 ? 4 : 2, &a);
+  return !a.c_tma || (p.residual && !a.r_tma);
+}
+
 // Which kernel: the least of these estimates, in microseconds, fitted to back-to-back calls
 // on B200 (148 SMs) over 1 <= M <= 25024, 300 <= N <= 4608, 512 <= K <= 4608; nkb = K / 128.
 //  * a 128-column K block of a 128 x 64 or 128 x 128 tile takes 0.33 us whatever its width
@@ -913,8 +919,8 @@ cudaError_t i8_run(const Int8Gemm& p, int num_sms, cudaStream_t st) {
     case kRows21: return i8_launch_rows<2, 1, T>(p, st);
     case kRows22: return i8_launch_rows<2, 2, T>(p, st);
     case kRows41: return i8_launch_rows<4, 1, T>(p, st);
-    case kTile: return i8_launch<128, false, T>(p, num_sms, st);
-    case kPairs: return i8_launch<256, true, T>(p, num_sms, st);
+    case kTile: return i8_launch<128, false, 64, T>(p, i8_words(p), num_sms, st);
+    case kPairs: return i8_pairs<T>(p, i8_words(p), num_sms, st);
     case kSplit64x2: return i8_launch_split<64, T>(p, 2, st);
     case kSplit64x4: return i8_launch_split<64, T>(p, 4, st);
     case kSplit128x2: return i8_launch_split<128, T>(p, 2, st);
