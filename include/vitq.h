@@ -288,7 +288,7 @@ int int8_gemm(const int8_t* A, int lda, const float* sA, const int8_t* W, int ld
 #define VITQ_ROPE_ADJACENT 4    /* pairs (2j, 2j+1) instead of (j, j + pairs) */
 #define VITQ_ROPE_INVERSE 8     /* turn back (by -angle): the gradient of the rotary */
 
-/* Layout of vit_rope_axes (host struct; strides in elements, all >= 0; the innermost
+/* Layout of vit_rope_axes (host struct; strides in elements, 0 .. 2^31 - 1; the innermost
  * dimension of a head is dense). */
 typedef struct {
   int32_t dtype;                      /* VITQ_BF16, VITQ_FP16 or VITQ_FP32, q and k alike */

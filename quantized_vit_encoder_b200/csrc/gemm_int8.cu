@@ -46,21 +46,19 @@ __device__ __forceinline__ void unpack16(const uint4& u, float* v) {
 #pragma unroll
   for (int i = 0; i < (int)(16 / sizeof(T)); ++i) v[i] = to_f32<T>(p[i]);
 }
-template <class T> __device__ __forceinline__ uint4 pack16(const float* v);
-template <> __device__ __forceinline__ uint4 pack16<float>(const float* v) {
-  return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+// Two values, the first in the low half.
+template <class T> __device__ __forceinline__ uint32_t round2(float lo, float hi);
+template <> __device__ __forceinline__ uint32_t round2<__nv_bfloat16>(float lo, float hi) { return pack_bf16x2(lo, hi); }
+template <> __device__ __forceinline__ uint32_t round2<__half>(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
-template <> __device__ __forceinline__ uint4 pack16<__nv_bfloat16>(const float* v) {
-  return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-}
-template <> __device__ __forceinline__ uint4 pack16<__half>(const float* v) {
-  uint4 u;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
-    (&u.x)[i] = *reinterpret_cast<const uint32_t*>(&h);
-  }
-  return u;
+template <class T>
+__device__ __forceinline__ uint4 pack16(const float* v) {
+  if constexpr (sizeof(T) == 4)
+    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+  else
+    return make_uint4(round2<T>(v[0], v[1]), round2<T>(v[2], v[3]), round2<T>(v[4], v[5]), round2<T>(v[6], v[7]));
 }
 
 // ------------------------------------------------------------------ tiles

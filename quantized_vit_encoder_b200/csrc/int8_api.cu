@@ -103,7 +103,7 @@ int vit_rope_axes(const vitq_rope_axes* p, const void* q, void* q_out, const voi
   VITQ_CHECK(pairs > 0 && 2 * pairs <= p->head_dim, VITQ_ERR_SHAPE);
   const int64_t strides[10] = {p->q_token,   p->q_head,     p->q_out_token, p->q_out_head, p->k_token,
                                p->k_head,    p->k_out_token, p->k_out_head, p->pos_token,  p->pos_axis};
-  for (int64_t v : strides) VITQ_CHECK(v >= 0 && v <= (1ll << 40), VITQ_ERR_SHAPE);
+  for (int64_t v : strides) VITQ_CHECK(v >= 0 && v < (1ll << 31), VITQ_ERR_SHAPE);
   // each output element is written once: one of the two strides spans the other's extent
   auto apart = [&](int64_t t, int64_t h, int heads) {
     return (h >= p->head_dim || heads <= 1) && (t >= (int64_t)(heads - 1) * h + p->head_dim || n_tokens <= 1) ? true
@@ -119,8 +119,8 @@ int vit_rope_axes(const vitq_rope_axes* p, const void* q, void* q_out, const voi
   VITQ_CHECK(al(q, es) && al(q_out, es) && al(k, es) && al(k_out, es) && al(pos, 4), VITQ_ERR_ALIGN);
 
   RopeAxes r = {};
-  r.side[0] = RopeSide{q, q_out, p->q_token, p->q_head, p->q_out_token, p->q_out_head, p->heads_q};
-  r.side[1] = RopeSide{k, k_out, p->k_token, p->k_head, p->k_out_token, p->k_out_head, p->heads_k};
+  r.side[0] = RopeSide{q, q_out, (int)p->q_token, (int)p->q_head, (int)p->q_out_token, (int)p->q_out_head, p->heads_q};
+  r.side[1] = RopeSide{k, k_out, (int)p->k_token, (int)p->k_head, (int)p->k_out_token, (int)p->k_out_head, p->heads_k};
   r.pos = pos;
   r.pos_t = p->pos_token;
   r.pos_a = p->pos_axis;
@@ -159,12 +159,13 @@ int vit_rope_axes(const vitq_rope_axes* p, const void* q, void* q_out, const voi
     double f = turn;
     for (int j = 0; j < pairs; ++j, f *= step) r.turns[j] = f;
   }
-  const int s = current_device_ok(nullptr);
+  int sms = 0;
+  const int s = current_device_ok(&sms);
   if (s) return s;
   if (n_tokens == 0 || p->heads_q + p->heads_k == 0) return VITQ_OK;
   VITQ_LAUNCH("rope_axes", S(stream), 0,
               2.0 * n_tokens * (p->heads_q + p->heads_k) * p->head_dim * es + 4.0 * n_tokens * p->n_axes,
-              launch_rope_axes(r, p->dtype, S(stream)));
+              launch_rope_axes(r, p->dtype, sms, S(stream)));
   return VITQ_OK;
 }
 

@@ -151,7 +151,7 @@ constexpr int kRopeMaxPairs = 256;
 struct RopeSide {
   const void* x;
   void* y;
-  long long xt, xh, yt, yh;   // token and head strides of input and output
+  int xt, xh, yt, yh;   // token and head strides of input and output
   int heads;
 };
 struct RopeAxes {
@@ -162,7 +162,7 @@ struct RopeAxes {
   double turns[kRopeMaxPairs];   // turns (angle / 2 pi) per position step
   uint8_t axis[kRopeMaxPairs];
 };
-cudaError_t launch_rope_axes(const RopeAxes& p, int dtype, cudaStream_t st);
+cudaError_t launch_rope_axes(const RopeAxes& p, int dtype, int num_sms, cudaStream_t st);
 
 cudaError_t launch_selftest_wait(int limit_us, cudaStream_t st);
 

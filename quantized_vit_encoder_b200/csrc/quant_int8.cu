@@ -136,6 +136,10 @@ __device__ __forceinline__ uint32_t pack4(uint32_t a, uint32_t b, uint32_t c, ui
   return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
 
+__device__ __noinline__ void store_codes_edge(int8_t* qc, uint2 w, int n) {
+  for (int i = 0; i < n; ++i) qc[i] = (int8_t)((i < 4 ? w.x : w.y) >> (8 * (i & 3)));
+}
+
 // Codes of one chunk at column col of a row with K columns.
 // (qc: where they go).  TAIL: the chunk may reach past K.
 template <class T, bool TAIL>
@@ -160,39 +164,54 @@ __device__ __forceinline__ void store_codes(const uint4& u, const RowScale& c, i
     if (PER == 8) *reinterpret_cast<uint2*>(qc) = make_uint2(w[0], w[PER / 4 - 1]);
     else *reinterpret_cast<uint32_t*>(qc) = w[0];
   } else {
-#pragma unroll
-    for (int i = 0; i < PER; ++i)
-      if (col + i < K) qc[i] = (int8_t)(w[i >> 2] >> (8 * (i & 3)));
+    store_codes_edge(qc, make_uint2(w[0], w[PER / 4 - 1]), K - col);
   }
 }
 
 // ---------------------------------------------------------------- loads
-// The chunk at column col of a row of K columns (zeros past K) from a row of any
-// alignment: 16 bytes at once where the row allows it, else 4-byte words, shifted by half
-// a word in rows that start on one.  Nothing outside the row is read.
+// The chunk at column col of a row of K columns (zeros past K), element by element.
 template <class T>
-__device__ __forceinline__ uint4 load_chunk_any(const T* xr, int col, int K) {
-  constexpr int PER = Elem<T>::PER;
+__device__ __noinline__ uint4 load_chunk_edge(const T* xr, int col, int K) {
   uint4 u = make_uint4(0u, 0u, 0u, 0u);
-  if (col + PER <= K) {
-    const uint32_t* p = reinterpret_cast<const uint32_t*>(reinterpret_cast<uintptr_t>(xr + col) & ~uintptr_t(3));
-    const uint32_t off = (uint32_t)reinterpret_cast<uintptr_t>(xr + col) & 15u;
-    if (off == 0) return *reinterpret_cast<const uint4*>(p);
-    if (PER == 4 || (off & 2u) == 0) return make_uint4(p[0], p[1], p[2], p[3]);
-    const uint16_t* h = reinterpret_cast<const uint16_t*>(xr + col);
-    const uint32_t w0 = col > 0 ? p[0] : (uint32_t)h[0] << 16, w1 = p[1], w2 = p[2], w3 = p[3];
-    const uint32_t w4 = col + PER < K ? p[4] : (uint32_t)h[7];
-    return make_uint4(__byte_perm(w0, w1, 0x5432), __byte_perm(w1, w2, 0x5432), __byte_perm(w2, w3, 0x5432),
-                      __byte_perm(w3, w4, 0x5432));
-  }
 #pragma unroll
-  for (int i = 0; i < PER; ++i) {
+  for (int i = 0; i < Elem<T>::PER; ++i) {
     if (col + i < K) {
-      if (PER == 8) (&u.x)[i >> 1] |= (uint32_t)reinterpret_cast<const uint16_t*>(xr)[col + i] << (16 * (i & 1));
+      if (sizeof(T) == 2) (&u.x)[i >> 1] |= (uint32_t)reinterpret_cast<const uint16_t*>(xr)[col + i] << (16 * (i & 1));
       else (&u.x)[i & 3] = reinterpret_cast<const uint32_t*>(xr)[col + i];
     }
   }
   return u;
+}
+
+// The same from a row of any alignment: put together from the one or two aligned 16-byte
+// units that its elements lie in (the second is the next thread's first).  Other bytes of
+// these units belong to the neighbouring rows; where there is none (lo_ok, hi_ok: a row
+// before, behind), chunks whose units reach past the matrix go element by element.
+template <class T>
+__device__ __forceinline__ uint4 load_chunk_any(const T* xr, int col, int K, bool lo_ok, bool hi_ok) {
+  constexpr int PER = Elem<T>::PER;
+  const uint32_t off = (uint32_t)reinterpret_cast<uintptr_t>(xr) & 15u;   // the same for all chunks of the row
+  const int lead = (int)(off / sizeof(T)), n = K - col;                   // elements before the chunk in its first unit
+  if ((lead && col == 0 && !lo_ok) || (!hi_ok && n < (lead ? 2 * PER - lead : PER))) return load_chunk_edge(xr, col, K);
+  const uint4* p = reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(xr + col) - off);
+  const uint4 a = p[0], b = lead && lead + n > PER ? p[1] : a;
+  uint32_t v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int i = 0; i < 6; ++i) v[i] = off & 8u ? v[i + 2] : v[i];
+#pragma unroll
+  for (int i = 0; i < 5; ++i) v[i] = off & 4u ? v[i + 1] : v[i];
+  if (sizeof(T) == 2) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = off & 2u ? __byte_perm(v[i], v[i + 1], 0x5432) : v[i];
+  }
+  if (n < PER) {   // zeros past K
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int left = n * (int)sizeof(T) - 4 * i;   // bytes of this word inside the row
+      v[i] = left >= 4 ? v[i] : left <= 0 ? 0u : v[i] & 0xFFFFu;
+    }
+  }
+  return make_uint4(v[0], v[1], v[2], v[3]);
 }
 
 // ---------------------------------------------------------------- row reductions
@@ -310,7 +329,7 @@ __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR)
     for (int c = 0; c < NC; ++c) {
       const int col = (c * TPR + t) * PER;
       u[c] = make_uint4(0u, 0u, 0u, 0u);
-      if (col < K) u[c] = ANY ? load_chunk_any(xt - t * PER, col, K) : *reinterpret_cast<const uint4*>(xt + c * TPR * PER);
+      if (col < K) u[c] = ANY ? load_chunk_any(xt - t * PER, col, K, row > 0, row < M - 1) : *reinterpret_cast<const uint4*>(xt + c * TPR * PER);
     }
     uint32_t m = 0u;
 #pragma unroll
@@ -403,7 +422,7 @@ __global__ void __launch_bounds__(TPR == 128 ? 128 : kLn8Threads, TPR == 128 ? 8
 #pragma unroll 3
     for (int c = 0, col = t * 8; c < nc; ++c, col += 8 * TPR, dst += 16 * pitch) {
       if (ANY) {
-        mine[c * pitch] = col < K ? load_chunk_any(xt - t * 8, col, K) : make_uint4(0u, 0u, 0u, 0u);
+        mine[c * pitch] = col < K ? load_chunk_any(xt - t * 8, col, K, r0 + sub > 0 && r0 > 0, r0 + sub < M - 1) : make_uint4(0u, 0u, 0u, 0u);
       } else {
         cp_async16(dst, col < K ? xt + c * (8 * TPR) : x, col < K ? 16u : 0u);
       }
@@ -416,8 +435,8 @@ __global__ void __launch_bounds__(TPR == 128 ? 128 : kLn8Threads, TPR == 128 ? 8
     const int col = i * 8;
     uint4 gu = make_uint4(0u, 0u, 0u, 0u), bu = gu;
     if (col < K) {
-      gu = wide ? *reinterpret_cast<const uint4*>(gamma + col) : load_chunk_any(gamma, col, K);
-      bu = wide ? *reinterpret_cast<const uint4*>(beta + col) : load_chunk_any(beta, col, K);
+      gu = wide ? *reinterpret_cast<const uint4*>(gamma + col) : load_chunk_any(gamma, col, K, false, false);
+      bu = wide ? *reinterpret_cast<const uint4*>(beta + col) : load_chunk_any(beta, col, K, false, false);
     }
     const int at = (2 * (i / TPR)) * TPR + i % TPR;
     sg[at] = make_float4(E::at(gu, 0), E::at(gu, 1), E::at(gu, 2), E::at(gu, 3));

@@ -73,7 +73,8 @@ def _close(got, x, pos, sections, **kw):
 CASES = [  # sections, head_dim, heads q, heads k
     ((12, 12, 12), 72, 16, 16), ((0, 18, 18), 72, 4, 2), ((24, 20, 20), 128, 8, 2), ((16, 24, 24), 128, 3, 1),
     ((9, 10, 11), 60, 2, 2), ((11, 11, 10), 64, 5, 1), ((1,), 2, 1, 1), ((3, 2), 16, 2, 1), ((7, 5, 4, 1), 40, 2, 3),
-    ((64, 0, 0), 256, 2, 2), ((128, 64, 64), 512, 1, 1), ((5,), 11, 3, 2)]
+    ((64, 0, 0), 256, 2, 2), ((128, 64, 64), 512, 1, 1), ((5,), 11, 3, 2),
+    ((1,), 511, 1, 2), ((64, 64, 127), 512, 2, 1), ((30, 30, 4), 200, 20, 7)]
 
 
 @pytest.mark.parametrize("t", [BF, HF, F32])

@@ -86,7 +86,7 @@ def _rope(**kw):
     (dict(sections=(0, 0, 0)), SHAPE), (dict(sections=(13, 12, 12)), SHAPE), (dict(head_dim=0), INVALID),
     (dict(head_dim=514), SHAPE), (dict(heads_q=-1), INVALID), (dict(heads_k=1025), SHAPE), (dict(flags=16), INVALID),
     (dict(theta=0.0), INVALID), (dict(theta=float("inf")), INVALID), (dict(theta=float("nan")), INVALID),
-    (dict(q=(-1, 72)), SHAPE), (dict(pos=(3, -1)), SHAPE),
+    (dict(q=(-1, 72)), SHAPE), (dict(pos=(3, -1)), SHAPE), (dict(q=(1 << 31, 72)), SHAPE),
     (dict(q_out=(72, 71)), SHAPE), (dict(q_out=(200, 72)), SHAPE), (dict(k_out=(0, 72)), SHAPE),
     # interleaved: axis 2 has no pair 2 + 3 * 12 in 36
     (dict(sections=(10, 13, 13), flags=vitq.ROPE_INTERLEAVED), SHAPE)])
