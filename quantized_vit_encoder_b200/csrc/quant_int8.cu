@@ -183,18 +183,37 @@ __device__ __noinline__ uint4 load_chunk_edge(const T* xr, int col, int K) {
   return u;
 }
 
-// The same from a row of any alignment: put together from the one or two aligned 16-byte
-// units that its elements lie in (the second is the next thread's first).  Other bytes of
-// these units belong to the neighbouring rows; where there is none (lo_ok, hi_ok: a row
-// before, behind), chunks whose units reach past the matrix go element by element.
+// Rows of any alignment: the aligned 16-byte units that a row lies in come to shared memory
+// by asynchronous copies, and a chunk is put together from two of them.  Other bytes of the
+// first and last unit belong to the neighbouring rows; the first row's first unit and the
+// last row's last one, which may have no neighbour, are read within the matrix only.
+__device__ __forceinline__ uint32_t row_off(const void* xr) { return (uint32_t)reinterpret_cast<uintptr_t>(xr) & 15u; }
+
+// Unit i of a row to dst.  off: bytes of unit 0 before the row.
 template <class T>
-__device__ __forceinline__ uint4 load_chunk_any(const T* xr, int col, int K, bool lo_ok, bool hi_ok) {
+__device__ __forceinline__ void fetch_unit(const T* xr, uint32_t off, int i, int K, bool first_row, bool last_row,
+                                           uint4* dst) {
   constexpr int PER = Elem<T>::PER;
-  const uint32_t off = (uint32_t)reinterpret_cast<uintptr_t>(xr) & 15u;   // the same for all chunks of the row
-  const int lead = (int)(off / sizeof(T)), n = K - col;                   // elements before the chunk in its first unit
-  if ((lead && col == 0 && !lo_ok) || (!hi_ok && n < (lead ? 2 * PER - lead : PER))) return load_chunk_edge(xr, col, K);
-  const uint4* p = reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(xr + col) - off);
-  const uint4 a = p[0], b = lead && lead + n > PER ? p[1] : a;
+  const char* from = reinterpret_cast<const char*>(xr) - off + (size_t)i * 16;
+  const int left = K * (int)sizeof(T) + (int)off - i * 16;   // bytes up to the end of the row
+  if (i == 0 && off && first_row) {
+    const int lead = (int)(off / sizeof(T));
+    uint4 u = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (int k = 1; k < PER; ++k) {
+      if (k >= lead && k - lead < K) {
+        if (sizeof(T) == 2) (&u.x)[k >> 1] |= (uint32_t)reinterpret_cast<const uint16_t*>(xr)[k - lead] << (16 * (k & 1));
+        else (&u.x)[k & 3] = reinterpret_cast<const uint32_t*>(xr)[k - lead];
+      }
+    }
+    *dst = u;
+  } else {
+    cp_async16(smem_u32(dst), from, last_row && left < 16 ? (uint32_t)left : 16u);
+  }
+}
+// The chunk at column col from its units a and b (off as above), zeros past K.
+template <class T>
+__device__ __forceinline__ uint4 chunk_of_units(const uint4& a, const uint4& b, uint32_t off, int col, int K) {
   uint32_t v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
   for (int i = 0; i < 6; ++i) v[i] = off & 8u ? v[i + 2] : v[i];
@@ -204,10 +223,10 @@ __device__ __forceinline__ uint4 load_chunk_any(const T* xr, int col, int K, boo
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = off & 2u ? __byte_perm(v[i], v[i + 1], 0x5432) : v[i];
   }
-  if (n < PER) {   // zeros past K
+  if (K - col < Elem<T>::PER) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int left = n * (int)sizeof(T) - 4 * i;   // bytes of this word inside the row
+      const int left = (K - col) * (int)sizeof(T) - 4 * i;   // bytes of this word inside the row
       v[i] = left >= 4 ? v[i] : left <= 0 ? 0u : v[i] & 0xFFFFu;
     }
   }
@@ -304,17 +323,19 @@ __device__ __forceinline__ uint4 gelu_chunk(const uint4& u, const uint32_t* lut)
 
 // ---------------------------------------------------------------- the row kernel
 // TPR threads per row, the row held in registers as at most NC chunks per thread, read
-// once.  ANY: rows of any alignment and K; otherwise whole 16-byte chunks.  Plain rows: one
-// CTA for each (or 8 rows, a warp each); GELU: persistent over the rows, since every CTA
-// stages the table.
+// once.  ANY: rows of any alignment and K, by way of shared memory (`units` 16-byte units a
+// row; the next row's are on their way while this one's codes are stored); otherwise whole
+// 16-byte chunks.  Plain rows: one CTA for each (or 8 rows, a warp each); GELU: persistent
+// over the rows, since every CTA stages the table.
 template <int OP, class T, int TPR, int NC, bool ANY>
 __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR)
-    rows_int8_kernel(const T* __restrict__ x, int ldx, int M, int K, int8_t* __restrict__ q, int ldq,
+    rows_int8_kernel(const T* __restrict__ x, int ldx, int M, int K, int units, int8_t* __restrict__ q, int ldq,
                      float* __restrict__ s) {
   constexpr int PER = Elem<T>::PER;
   constexpr int ROWS = TPR == 32 ? 8 : 1;
   __shared__ uint32_t sh_max[32];
   __shared__ __align__(16) uint32_t lut[OP == kI8Gelu ? kGeluN : 1];
+  extern __shared__ uint4 row_units[];   // ANY
   pdl_trigger();
   if (OP == kI8Gelu) {   // the table is this library's own, written before its first launch
     gelu_stage(lut);
@@ -322,14 +343,36 @@ __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR)
   }
   pdl_wait();
   const int t = TPR == 32 ? threadIdx.x & 31 : threadIdx.x;
-  for (int row = blockIdx.x * ROWS + (TPR == 32 ? threadIdx.x >> 5 : 0); row < M; row += gridDim.x * ROWS) {
-    const T* xt = x + (size_t)row * ldx + t * PER;   // whole warps (TPR = 32) or whole CTAs share a row
+  uint4* mine = row_units + (TPR == 32 ? (threadIdx.x >> 5) * units : 0);
+  auto fetch = [&](int row) {
+    const T* xr = x + (size_t)row * ldx;
+    const uint32_t off = row_off(xr);
+    const int n = (K * (int)sizeof(T) + (int)off + 15) / 16;
+    for (int i = t; i < n; i += TPR) fetch_unit(xr, off, i, K, row == 0, row == M - 1, mine + i);
+    cp_async_commit();
+  };
+  // whole warps (TPR = 32) or whole CTAs share a row
+  int row = blockIdx.x * ROWS + (TPR == 32 ? threadIdx.x >> 5 : 0);
+  if (ANY && row < M) fetch(row);
+  for (; row < M; row += gridDim.x * ROWS) {
+    const T* xt = x + (size_t)row * ldx + t * PER;
     uint4 u[NC];
+    if (ANY) {
+      cp_async_wait<0>();
+      if (TPR == 32) __syncwarp();
+      else __syncthreads();
+      const uint32_t off = row_off(xt - t * PER);
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      const int col = (c * TPR + t) * PER;
-      u[c] = make_uint4(0u, 0u, 0u, 0u);
-      if (col < K) u[c] = ANY ? load_chunk_any(xt - t * PER, col, K, row > 0, row < M - 1) : *reinterpret_cast<const uint4*>(xt + c * TPR * PER);
+      for (int c = 0; c < NC; ++c) {
+        const int i = c * TPR + t, col = i * PER;
+        u[c] = col < K ? chunk_of_units<T>(mine[i], mine[i + 1], off, col, K) : make_uint4(0u, 0u, 0u, 0u);
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        u[c] = make_uint4(0u, 0u, 0u, 0u);
+        if ((c * TPR + t) * PER < K) u[c] = *reinterpret_cast<const uint4*>(xt + c * TPR * PER);
+      }
     }
     uint32_t m = 0u;
 #pragma unroll
@@ -337,7 +380,8 @@ __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR)
       if (OP == kI8Gelu && (c * TPR + t) * PER < K) u[c] = gelu_chunk(u[c], lut);
       m = max(m, chunk_mag<T>(u[c]));
     }
-    const RowScale sc = row_scale<T>(row_max<TPR>(m, sh_max));
+    const RowScale sc = row_scale<T>(row_max<TPR>(m, sh_max));   // every thread has its chunks in registers now
+    if (ANY && row + (int)gridDim.x * ROWS < M) fetch(row + gridDim.x * ROWS);
     int8_t* qt = q + (size_t)row * ldq + t * PER;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
@@ -393,7 +437,7 @@ __device__ __noinline__ uint4 ln_chunk_exact(const uint4 v, const float4* g, con
 constexpr int kLn8Threads = 256;
 
 // nc chunks a thread (nc * TPR * 8 >= K).  TPR = 128: 128 threads a CTA.
-// ANY: rows of any alignment and K, loaded synchronously.
+// ANY: rows of any alignment and K.
 template <int TPR, bool ANY>
 __global__ void __launch_bounds__(TPR == 128 ? 128 : kLn8Threads, TPR == 128 ? 8 : 4)
     ln_rows_int8_kernel(const __nv_bfloat16* __restrict__ x, int ldx, int M, int K, int nc,
@@ -417,15 +461,17 @@ __global__ void __launch_bounds__(TPR == 128 ? 128 : kLn8Threads, TPR == 128 ? 8
   const int stride = gridDim.x * rows;
   const uint32_t mine_s = smem_u32(mine);
   auto fetch = [&](int r0) {   // a spare half warp repeats its neighbour's row
-    const __nv_bfloat16* xt = x + (size_t)(r0 + sub < M ? r0 + sub : r0) * ldx + t * 8;
-    uint32_t dst = mine_s;
+    const int r = r0 + sub < M ? r0 + sub : r0;
+    const __nv_bfloat16* xt = x + (size_t)r * ldx + t * 8;
+    if constexpr (ANY) {   // the row's units; unit i has the place of chunk i
+      const uint32_t off = row_off(xt - t * 8);
+      const int n = (K * 2 + (int)off + 15) / 16;
+      for (int c = 0, i = t; i < n; ++c, i += TPR) fetch_unit(xt - t * 8, off, i, K, r == 0, r == M - 1, mine + c * pitch);
+    } else {
+      uint32_t dst = mine_s;
 #pragma unroll 3
-    for (int c = 0, col = t * 8; c < nc; ++c, col += 8 * TPR, dst += 16 * pitch) {
-      if (ANY) {
-        mine[c * pitch] = col < K ? load_chunk_any(xt - t * 8, col, K, r0 + sub > 0 && r0 > 0, r0 + sub < M - 1) : make_uint4(0u, 0u, 0u, 0u);
-      } else {
+      for (int c = 0, col = t * 8; c < nc; ++c, col += 8 * TPR, dst += 16 * pitch)
         cp_async16(dst, col < K ? xt + c * (8 * TPR) : x, col < K ? 16u : 0u);
-      }
     }
     cp_async_commit();
   };
@@ -435,8 +481,8 @@ __global__ void __launch_bounds__(TPR == 128 ? 128 : kLn8Threads, TPR == 128 ? 8
     const int col = i * 8;
     uint4 gu = make_uint4(0u, 0u, 0u, 0u), bu = gu;
     if (col < K) {
-      gu = wide ? *reinterpret_cast<const uint4*>(gamma + col) : load_chunk_any(gamma, col, K, false, false);
-      bu = wide ? *reinterpret_cast<const uint4*>(beta + col) : load_chunk_any(beta, col, K, false, false);
+      gu = wide ? *reinterpret_cast<const uint4*>(gamma + col) : load_chunk_edge(gamma, col, K);
+      bu = wide ? *reinterpret_cast<const uint4*>(beta + col) : load_chunk_edge(beta, col, K);
     }
     const int at = (2 * (i / TPR)) * TPR + i % TPR;
     sg[at] = make_float4(E::at(gu, 0), E::at(gu, 1), E::at(gu, 2), E::at(gu, 3));
@@ -466,6 +512,22 @@ __global__ void __launch_bounds__(TPR == 128 ? 128 : kLn8Threads, TPR == 128 ? 8
   for (; row0 < M; row0 += stride) {
     const int row = row0 + sub;
     cp_async_wait<0>();
+    if (ANY) {   // units to chunks, in place: a chunk's second unit is the next thread's, or the next chunk's first
+      const uint32_t off = row_off(x + (size_t)(row < M ? row : row0) * ldx);
+      const int n = (K * 2 + (int)off + 15) / 16;
+      const uint4* next = t + 1 < TPR ? mine + 1 : mine + 1 - TPR + pitch;
+#pragma unroll 1
+      for (int c = 0; c < nc; ++c) {
+        const int i = c * TPR + t;
+        if (TPR > 32) __syncthreads();
+        else __syncwarp();
+        uint4 u = make_uint4(0u, 0u, 0u, 0u);
+        if (i * 8 < K) u = chunk_of_units<__nv_bfloat16>(mine[c * pitch], i + 1 < n ? next[c * pitch] : u, off, i * 8, K);
+        if (TPR > 32) __syncthreads();
+        else __syncwarp();
+        mine[c * pitch] = u;
+      }
+    }
     double s1 = 0.0, s2 = 0.0, t1 = 0.0, t2 = 0.0;
 #pragma unroll 3
     for (int c = 0; c < nc; ++c) {
@@ -624,9 +686,16 @@ cudaError_t rows_launch(const RowsInt8& a, int num_sms, cudaStream_t st) {
     const long long most = (long long)num_sms * (TPR == 32 ? 3 : TPR >= 1024 ? 1 : 896 / TPR);
     if (grid > most) grid = most;
   }
-  auto kern = rows_whole<T>(a) ? rows_int8_kernel<OP, T, TPR, NC, false> : rows_int8_kernel<OP, T, TPR, NC, true>;
-  return launch_pdl(kern, dim3((unsigned)grid), dim3(TPR == 32 ? 256 : TPR), 0, st, (const T*)a.x, a.ldx, a.M, a.K,
-                    a.q, a.ldq, a.s);
+  const bool whole = rows_whole<T>(a);
+  auto kern = whole ? rows_int8_kernel<OP, T, TPR, NC, false> : rows_int8_kernel<OP, T, TPR, NC, true>;
+  const int units = (a.K * (int)sizeof(T) + 15) / 16 + 2;   // a row in units it may not start on, and one behind
+  const size_t smem = whole ? 0 : (size_t)units * 16 * (TPR == 32 ? 8 : 1);
+  if (smem > 32 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_pdl(kern, dim3((unsigned)grid), dim3(TPR == 32 ? 256 : TPR), smem, st, (const T*)a.x, a.ldx, a.M, a.K,
+                    units, a.q, a.ldq, a.s);
 }
 
 template <int OP, class T>
@@ -641,7 +710,8 @@ cudaError_t ln_rows_launch(const RowsInt8& a, int num_sms, cudaStream_t st) {
   // as many threads a CTA as leave every SM one (gamma and beta are staged once a CTA)
   int threads = TPR == 128 ? 128 : kLn8Threads;
   while (threads > 32 && TPR < 128 && (long long)num_sms * threads / TPR > a.M) threads /= 2;
-  const size_t smem = (size_t)nc * 16 * (4 * TPR + threads);
+  // (one more row of chunks for the unit behind the last in rows that start inside one)
+  const size_t smem = (size_t)nc * 16 * (4 * TPR + threads) + (rows_whole<__nv_bfloat16>(a) ? 0 : 16 * threads);
   auto kern = rows_whole<__nv_bfloat16>(a) ? ln_rows_int8_kernel<TPR, false> : ln_rows_int8_kernel<TPR, true>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
