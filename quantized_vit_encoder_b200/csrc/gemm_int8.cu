@@ -295,10 +295,10 @@ __device__ void i8_epilogue(const I8Smem<Cfg>& sm, uint32_t tmem_base, const I8A
 #pragma unroll
     for (int c = lane; c < Cfg::COLS; c += 32) {
       const int n = col0 + c;
-      sw_s[c] = n < g.N ? __ldg(g.sW + n) : 0.f;
+      sw_s[c] = n < g.N ? g.sW[n] : 0.f;
       bias_s[c] = bias && n < g.N ? to_f32<T>(bias[n]) : 0.f;
     }
-    const float sa = row < g.M ? __ldg(g.sA + row) : 0.f;
+    const float sa = row < g.M ? g.sA[row] : 0.f;
     const uint64_t sa2 = f2pack(sa, sa);
     __syncwarp();
     bool ok = mbar_wait(sm.tfull(acc), (it / Cfg::NACC) & 1u, sm.abort_flag());
@@ -512,15 +512,23 @@ __device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, ui
 // 16 codes of a weight row (used once: not kept in L1).
 __device__ __forceinline__ uint4 ld_once(const int8_t* p) {
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+  return v;
+}
+// The last n < 16 codes of a row, zeros behind them.
+__device__ __noinline__ uint4 ld_last(const int8_t* p, int n) {
+  uint4 v = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+  for (int i = 0; i < 15; ++i)
+    if (i < n) (&v.x)[i >> 2] |= (uint32_t)(uint8_t)p[i] << (8 * (i & 3));
   return v;
 }
 
 // NT: groups of 8 tokens, CT: groups of 16 channels of a CTA; gridDim.y covers more tokens.
 template <int NT, int CT, class T>
 __global__ void __launch_bounds__(32 * kRowsWarps)
-    int8_gemm_rows_kernel(const int8_t* __restrict__ A, int lda, const int8_t* __restrict__ W, int ldw, const I8Args g) {
+    int8_gemm_rows_kernel(const int8_t* A, int lda, const int8_t* W, int ldw, const I8Args g) {
   constexpr int U = NT + 2 * CT <= 4 ? 4 : NT + 2 * CT <= 6 ? 3 : 2;   // pieces of K in flight
   constexpr int CH = 16 * CT;
   __shared__ int part[kRowsWarps][NT * 8][CH + 1];
@@ -540,26 +548,22 @@ __global__ void __launch_bounds__(32 * kRowsWarps)
   for (int k = warp * 64; k < g.K; k += U * 64 * kRowsWarps) {
     uint4 u[U][2 * CT], b[U][NT];
 #pragma unroll
-    for (int i = 0; i < U; ++i) {   // codes past K lie within the padded rows (16-byte pitch)
+    for (int i = 0; i < U; ++i) {
       const int kk = k + i * 64 * kRowsWarps;
-      const bool in = kk + t * 16 < g.K;
+      const bool in = kk + t * 16 + 16 <= g.K;
 #pragma unroll
       for (int c = 0; c < 2 * CT; ++c) u[i][c] = in ? ld_once(w[c] + kk) : zero;
 #pragma unroll
-      for (int j = 0; j < NT; ++j) b[i][j] = in ? __ldg(reinterpret_cast<const uint4*>(a[j] + kk)) : zero;
+      for (int j = 0; j < NT; ++j) b[i][j] = in ? *reinterpret_cast<const uint4*>(a[j] + kk) : zero;
     }
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      const int left = g.K - (k + i * 64 * kRowsWarps + t * 16);   // codes of this piece inside K
-      if (left > 0 && left < 16) {   // the tokens' codes past K count as zero
+      const int kk = k + i * 64 * kRowsWarps, left = g.K - (kk + t * 16);   // codes of this piece inside K
+      if (left > 0 && left < 16) {
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
+        for (int c = 0; c < 2 * CT; ++c) u[i][c] = ld_last(w[c] + kk, left);
 #pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            const int keep = left - 4 * h;
-            uint32_t& v = (&b[i][j].x)[h];
-            v = keep >= 4 ? v : keep <= 0 ? 0u : v & ((1u << (8 * keep)) - 1u);
-          }
+        for (int j = 0; j < NT; ++j) b[i][j] = ld_last(a[j] + kk, left);
       }
 #pragma unroll
       for (int c = 0; c < CT; ++c)
@@ -584,7 +588,7 @@ __global__ void __launch_bounds__(32 * kRowsWarps)
     int sum = 0;
 #pragma unroll
     for (int x = 0; x < kRowsWarps; ++x) sum += part[x][e / CH][c];
-    float v = __fmaf_rn(__fmul_rn(__int2float_rn(sum), __ldg(g.sA + m)), __ldg(g.sW + n),
+    float v = __fmaf_rn(__fmul_rn(__int2float_rn(sum), g.sA[m]), g.sW[n],
                         g.bias ? to_f32<T>(reinterpret_cast<const T*>(g.bias)[n]) : 0.f);
     if (g.residual) v += to_f32<T>(reinterpret_cast<const T*>(g.residual)[(size_t)m * g.ldr + n]);
     reinterpret_cast<T*>(g.C)[(size_t)m * g.ldc + n] = of_f32<T>(v);
@@ -720,10 +724,10 @@ __global__ void __launch_bounds__(SplitCfg::THREADS, 1)
     // what the epilogue will need, on its way while the products run
     if (threadIdx.x - 128 < cols) {
       const int c = threadIdx.x - 128, n = n0 + c_first + c;
-      sw_s[c] = n < g.N ? __ldg(g.sW + n) : 0.f;
+      sw_s[c] = n < g.N ? g.sW[n] : 0.f;
       bias_s[c] = g.bias && n < g.N ? to_f32<T>(reinterpret_cast<const T*>(g.bias)[n]) : 0.f;
     }
-    if (row_in) sa = __ldg(g.sA + row);
+    if (row_in) sa = g.sA[row];
 #pragma unroll
     for (int k = 0; k < UNITS; ++k) {
       const int u = half + 2 * k, n = n0 + c_first + u * 8;
@@ -904,6 +908,7 @@ I8Kernel i8_choose(int M, int N, int K, int num_sms) {
   auto rows = [&](I8Kernel k, int tokens, int channels) {
     offer(k, 2.0 + 1.35e-7 * (nk * ((M + tokens - 1) / tokens) + nk / channels * M));
   };
+  if (M > 1024) return best;   // (the kernel for few rows would have too many row groups for a grid)
   if (M > 64) rows(kRows41, 32, 16);
   else if (M > 16 && N >= 32 * 128) rows(kRows22, 16, 32);
   else rows(kRows21, 16, 16);

@@ -6,6 +6,9 @@
 // with the exact quotient by the fp32 number s.  A zero s (amax 0, or below
 // 127 * 2^-150) gives zero codes; a row holding an infinity or a NaN gets
 // s = NaN and zero codes, so that its row of a product comes out NaN.
+//
+// (No __restrict__ and no __ldg on what an earlier kernel may have written: such loads could
+// be moved before the wait for that kernel.)
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -329,8 +332,8 @@ __device__ __forceinline__ uint4 gelu_chunk(const uint4& u, const uint32_t* lut)
 // over the rows, since every CTA stages the table.
 template <int OP, class T, int TPR, int NC, bool ANY>
 __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR)
-    rows_int8_kernel(const T* __restrict__ x, int ldx, int M, int K, int units, int8_t* __restrict__ q, int ldq,
-                     float* __restrict__ s) {
+    rows_int8_kernel(const T* x, int ldx, int M, int K, int units, int8_t* q, int ldq,
+                     float* s) {
   constexpr int PER = Elem<T>::PER;
   constexpr int ROWS = TPR == 32 ? 8 : 1;
   __shared__ uint32_t sh_max[32];
@@ -440,9 +443,9 @@ constexpr int kLn8Threads = 256;
 // ANY: rows of any alignment and K.
 template <int TPR, bool ANY>
 __global__ void __launch_bounds__(TPR == 128 ? 128 : kLn8Threads, TPR == 128 ? 8 : 4)
-    ln_rows_int8_kernel(const __nv_bfloat16* __restrict__ x, int ldx, int M, int K, int nc,
-                        const __nv_bfloat16* __restrict__ gamma, const __nv_bfloat16* __restrict__ beta, double eps,
-                        int8_t* __restrict__ q, int ldq, float* __restrict__ s) {
+    ln_rows_int8_kernel(const __nv_bfloat16* x, int ldx, int M, int K, int nc,
+                        const __nv_bfloat16* gamma, const __nv_bfloat16* beta, double eps,
+                        int8_t* q, int ldq, float* s) {
   using E = Elem<__nv_bfloat16>;
   constexpr int LANES = TPR < 32 ? TPR : 32;
   extern __shared__ float4 ln8_smem[];     // gamma, beta: chunk c of thread t at (2c + half) * TPR + t; then the chunks
@@ -637,9 +640,9 @@ __device__ __forceinline__ float value_of_bits(uint32_t b) {
 
 template <int OP, class T>
 __global__ void __launch_bounds__(kAnyThreads)
-    rows_int8_any_kernel(const T* __restrict__ x, int ldx, int M, int K, const __nv_bfloat16* __restrict__ gamma,
-                         const __nv_bfloat16* __restrict__ beta, double eps, int8_t* __restrict__ q, int ldq,
-                         float* __restrict__ s) {
+    rows_int8_any_kernel(const T* x, int ldx, int M, int K, const __nv_bfloat16* gamma,
+                         const __nv_bfloat16* beta, double eps, int8_t* q, int ldq,
+                         float* s) {
   __shared__ double sh_sum[32];
   __shared__ uint32_t sh_max[32];
   pdl_trigger();

@@ -368,7 +368,7 @@ _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}   # VITQ_BF16,
 _BF16_ONLY, _I8_ONLY, _F32_ONLY = (_bf16,), (torch.int8,), (_f32,)
 
 # The kernels behind these calls take a few microseconds at small sizes, so their checks read each property of a
-# tensor once and allocate with new_empty; a call that fails a check is explained by _why.
+# tensor once; a call that fails a check is explained by _why.
 
 
 def _device(t, name):
@@ -425,20 +425,20 @@ def _vec(t, name, dev, dtype, n):
     return t.data_ptr()
 
 
-def _new(like, shape, dtype, stream):
-    """An output tensor, allocated for the stream that the kernel runs on."""
+def _new(like, shape, strides, dtype, stream):
+    """An output tensor, allocated for the stream that the kernel runs on (empty_strided: the quickest of torch's
+    allocations, 1.6 us against 2.0 to 2.4)."""
     if stream is None:
-        return like.new_empty(shape, dtype=dtype)
+        return torch.empty_strided(shape, strides, dtype=dtype, device=like.device)
     with torch.cuda.stream(stream):
-        return like.new_empty(shape, dtype=dtype)
+        return torch.empty_strided(shape, strides, dtype=dtype, device=like.device)
 
 
 def _codes_out(out, x, dev, m, k, stream):
     """The (codes, scales, row stride) to write: given, or new ones with a row stride of a multiple of 16."""
     if out is None:
         ldq = (k + 15) // 16 * 16
-        q = _new(x, (m, ldq), torch.int8, stream)
-        return (q if ldq == k else q[:, :k]), _new(x, (m,), _f32, stream), ldq
+        return _new(x, (m, k), (ldq, 1), torch.int8, stream), _new(x, (m,), (1,), _f32, stream), ldq
     q, s = out
     ldq = _mat(q, "out codes", dev, _I8_ONLY, m, k)[2]
     _vec(s, "out scales", dev, _f32, m)
@@ -498,7 +498,7 @@ def int8_gemm(qa, sa, qw, sw, bias=None, residual=None, out=None, out_dtype=torc
         ldr = _mat(residual, "residual", dev, (out_dtype,), m, n)[2]
         res_p = residual.data_ptr()
     if out is None:
-        out = _new(qa, (m, n), out_dtype, stream)
+        out = _new(qa, (m, n), (n, 1), out_dtype, stream)
     _check(load().int8_gemm(qa.data_ptr(), lda, sa_p, qw.data_ptr(), ldw, sw_p, bias_p, res_p, ldr, out.data_ptr(),
                             ldc, _DTYPES[out_dtype], m, n, k, _raw(stream, dev)), "int8_gemm")
     return out
@@ -538,9 +538,9 @@ def rope_axes(q, k, pos, sections, theta: float = 10000.0, interleaved: bool = F
         _, hk, _, kt, kh = _heads(k, "k", dev, (t,), n, None, d)
         k_p = k.data_ptr()
     if out is None:
-        qo, qot, qoh = _new(q, (n, hq, d), t, stream), hq * d, d
+        qo, qot, qoh = _new(q, (n, hq, d), (hq * d, d, 1), t, stream), hq * d, d
         if k is not None:
-            ko, kot, koh = _new(q, (n, hk, d), t, stream), hk * d, d
+            ko, kot, koh = _new(q, (n, hk, d), (hk * d, d, 1), t, stream), hk * d, d
     else:
         qo, ko = out
         qot, qoh = _heads(qo, "out q", dev, (t,), n, hq, d)[3:]

@@ -127,6 +127,40 @@ def test_quant_every_bf16_pair_of_significands():
         _same(vitq.quant_int8(xs), _codes_ref(xs), scale)
 
 
+@pytest.mark.parametrize("dtype", [BF, HF, F32])
+@pytest.mark.parametrize("start", [0, 1, 3, 7])
+@pytest.mark.parametrize("M,K", [(1, 1), (1, 5), (1, 17), (2, 9), (3, 1203), (2, 4303), (9, 40)])
+def test_quant_rows_that_fill_their_storage(M, K, start, dtype):
+    """Rows that start anywhere in a 16-byte unit, first and last row at the ends of the storage."""
+    buf = torch.empty(start + M * K, dtype=dtype, device="cuda")
+    x = buf[start:].view(M, K)
+    x.copy_(_randn(K + start, M, K))
+    _same(vitq.quant_int8(x), _codes_ref(x))
+    if dtype == BF:
+        g, b = (1 + 0.1 * _randn(1, K)).to(BF), (0.1 * _randn(2, K)).to(BF)
+        _same(vitq.ln_quant_int8(x, g, b), _codes_ref(_ln_ref(x, g, b, 1e-6)))
+        _same(vitq.gelu_quant_int8(x), _codes_ref(_gelu_ref(x)))
+
+
+@pytest.mark.parametrize("K", [65535, 65536, 20001, 16392, 16376, 2305, 1160])
+def test_widest_rows(K):
+    for dtype in (BF, HF, F32):
+        x = _randn(K, 3, K).to(dtype)
+        _same(vitq.quant_int8(x), _codes_ref(x), (K, dtype))
+    x = (_randn(K, 3, K) + 0.5).to(BF)
+    g, b = (1 + 0.1 * _randn(1, K)).to(BF), (0.1 * _randn(2, K)).to(BF)
+    _same(vitq.ln_quant_int8(x, g, b), _codes_ref(_ln_ref(x, g, b, 1e-6)), K)
+    _same(vitq.gelu_quant_int8(x), _codes_ref(_gelu_ref(x)), K)
+
+
+def test_ln_quant_unaligned_gamma_and_beta():
+    K = 1152
+    x = _randn(1, 50, K).to(BF)
+    gb = (1 + 0.1 * _randn(2, 2 * K + 3)).to(BF)
+    gamma, beta = gb[1:K + 1], gb[K + 2:2 * K + 2]
+    _same(vitq.ln_quant_int8(x, gamma, beta), _codes_ref(_ln_ref(x, gamma, beta, 1e-6)))
+
+
 def test_quant_leaves_the_rest_of_its_outputs():
     x = _randn(3, 5, 100).to(BF)
     buf, s = torch.full((7, 128), 99, dtype=torch.int8, device="cuda"), torch.full((7,), -1.0, device="cuda")
@@ -272,6 +306,47 @@ def test_gemm_bias_and_residual(M, N, K, t):
     _gemm_check(M, N, K, t, bias=True)
     _gemm_check(M, N, K, t, bias=True, residual=True)
     _gemm_check(M, N, K, t, residual=True)
+
+
+# shapes for each kernel behind int8_gemm: few rows (by 8, 16, 16 x 32 channels, 32), a tile split over
+# 2, 4 and 8 CTAs at both widths, single tiles, pairs with short and long sums; whole and odd N and K
+VARIANTS = [(8, 64, 200), (7, 4607, 4603), (16, 2048, 1000), (33, 1152, 1152), (40, 4200, 1152), (24, 4608, 4608),
+            (100, 100, 700), (128, 512, 512), (127, 515, 509), (64, 4608, 4608), (129, 900, 4304), (512, 2048, 4608),
+            (500, 2049, 4607), (243, 2048, 4608), (250, 2043, 4601), (128, 1152, 4304), (121, 1101, 5001),
+            (300, 4304, 1152), (301, 4303, 1151), (2000, 300, 300), (5000, 2688, 200), (5001, 2689, 203),
+            (2100, 1156, 1100), (3001, 2690, 900), (70000, 8, 16)]
+
+
+@pytest.mark.parametrize("t", [BF, HF, F32])
+@pytest.mark.parametrize("M,N,K", VARIANTS)
+def test_gemm_every_kernel(M, N, K, t):
+    _gemm_check(M, N, K, t, bias=True, residual=True)
+
+
+@pytest.mark.parametrize("M,N,K", [(5, 40, 50), (20, 40, 50), (130, 40, 50), (300, 264, 205)])
+def test_gemm_operands_that_end_with_their_last_row(M, N, K):
+    """Row pitch 64 (208), but storage that ends right behind the last row's last code."""
+    ld = (K + 15) // 16 * 16
+    qa, qw = _i8(1, M, K), _i8(2, N, K)
+    def tight(q):
+        buf = torch.zeros((q.shape[0] - 1) * ld + K, dtype=torch.int8, device="cuda")
+        v = buf.as_strided(q.shape, (ld, 1))
+        v.copy_(q)
+        return v
+    sa, sw = torch.rand(M, device="cuda"), torch.rand(N, device="cuda")
+    assert torch.equal(vitq.int8_gemm(tight(qa), sa, tight(qw), sw), vitq.int8_gemm(qa, sa, qw, sw))
+
+
+@pytest.mark.parametrize("M", [2, 40, 150, 700])
+def test_gemm_largest_width(M):
+    """N and K at the entry point's limit (65536), rows of weights of one shared value."""
+    N, K = 65536, 64
+    qa = _i8(1, M, K)
+    qw = _i8(2, N, K)
+    sa, sw = torch.rand(M, device="cuda"), torch.rand(N, device="cuda")
+    y = vitq.int8_gemm(qa, sa, qw, sw, out_dtype=F32)
+    want = (qa.double() @ qw.double().t()) * sa.double()[:, None] * sw.double()
+    assert ((y.double() - want).abs() <= 4 * 2.0 ** -24 * want.abs()).all()
 
 
 @pytest.mark.parametrize("M,N,K", [(6256, 1152, 1152), (2500, 3456, 1152), (1564, 4608, 4608)])
