@@ -5,7 +5,16 @@
 // One scale per token and per output channel: nothing changes along K, so the
 // whole sum stays in TMEM as exact 32-bit integers (K <= 2^16 and |code| <= 128
 // keep it below 2^31) and the scales are applied once per output, in fp32, before
-// the one rounding to T.
+// the one rounding to T.  The sums being exact, every kernel below gives the same bits:
+//   few rows    M <= 1024   mma.sync, weights streamed once; bound by L2 / HBM bytes
+//   split K     M <= 1024   128 x 64 / 128 tiles, a cluster's CTAs share K; bound by latency
+//   tiles       128 x 128, one CTA each, persistent
+//   pairs       256 x 256, two CTAs each, persistent; bound by the tensor cores
+// 25024 x 3456 x 1152 (pairs, bf16): 84 .. 87 us in short runs, 98 .. 104 under the power
+// limit, against 62 .. 64 at the measured FP8 rate (3125 TFLOP/s); the tensor pipe is busy
+// half of the time.  A K block of a pair takes about 780 cycles without loads or epilogue.
+// 6256 x 1152 x 4304 with residual: 35.7 us (19.3).  243 x 2048 x 4608: 10.4.
+// 1 x 4608 x 4608: 6.0, 21 MB of weights at 3.5 TB/s.
 #include "internal.h"
 #include "ptx.cuh"
 

@@ -68,14 +68,14 @@ __device__ __forceinline__ uint32_t chunk_mag(const uint4& u) {
 // ---------------------------------------------------------------- codes of a row
 // How the codes of a row come from its scale s.  With s >= 2^-107 the product
 // p = y * r, r = fl32(1 / s), is within 2^-23 (relative) of y / s.  For bf16 values p
-// (not rounded itself: one FMA adds it to 1.5 2^23, whose spacing is 1) rounds like y / s once r is moved by 2^-21 in the right direction: with the 8-bit
-// significands Y of y and A of amax, amax / 127 against y / (k + 1/2) is a comparison
-// of 254 Y 2^i with (2k + 1) A 2^j, integers below 2^16 times one power of two.
-// Either they differ by 2^-16 of their size, which the move and the roundings cannot
-// cross, or they are equal.  Equality needs 127 | A, and then s is a power of two, r
-// and p are exact and p rounds ties to even itself; or 127 | 2k + 1, so |y| = amax / 2,
-// and the sign of amax/2 - 63.5 s (one FMA, exact sign) says to which side of 63.5 the
-// quotient falls and r moves.
+// (not rounded itself: one FMA adds it to 1.5 2^23, whose spacing is 1) rounds like y / s
+// once r is moved by 2^-21 in the right direction: with the 8-bit significands Y of y and A
+// of amax, amax / 127 against y / (k + 1/2) is a comparison of 254 Y 2^i with
+// (2k + 1) A 2^j, integers below 2^16 times one power of two.  Either they differ by 2^-16
+// of their size, which the move and the roundings cannot cross, or they are equal.
+// Equality needs 127 | A, and then s is a power of two, r and p are exact and p rounds ties
+// to even itself; or 127 | 2k + 1, so |y| = amax / 2, and the sign of amax/2 - 63.5 s (one
+// FMA, exact sign) says to which side of 63.5 the quotient falls and r moves.
 // fp16 and fp32 values have more exact ties: where p lies within 2^-14 of one, the
 // sign of y - h s decides.  Rows with a smaller scale (amax < 127 * 2^-107) divide in
 // fp64.
@@ -143,8 +143,8 @@ __device__ __noinline__ void store_codes_edge(int8_t* qc, uint2 w, int n) {
   for (int i = 0; i < n; ++i) qc[i] = (int8_t)((i < 4 ? w.x : w.y) >> (8 * (i & 3)));
 }
 
-// Codes of one chunk at column col of a row with K columns.
-// (qc: where they go).  TAIL: the chunk may reach past K.
+// Codes of one chunk at column col of a row with K columns, to qc.  TAIL: the chunk may
+// reach past K.
 template <class T, bool TAIL>
 __device__ __forceinline__ void store_codes(const uint4& u, const RowScale& c, int8_t* qc, int col, int K) {
   constexpr int PER = Elem<T>::PER;
@@ -159,9 +159,9 @@ __device__ __forceinline__ void store_codes(const uint4& u, const RowScale& c, i
     }
   } else {
 #pragma unroll
-  for (int g = 0; g < PER / 4; ++g)
-    w[g] = pack4(code_of<T>(Elem<T>::at(u, 4 * g), c), code_of<T>(Elem<T>::at(u, 4 * g + 1), c),
-                 code_of<T>(Elem<T>::at(u, 4 * g + 2), c), code_of<T>(Elem<T>::at(u, 4 * g + 3), c));
+    for (int g = 0; g < PER / 4; ++g)
+      w[g] = pack4(code_of<T>(Elem<T>::at(u, 4 * g), c), code_of<T>(Elem<T>::at(u, 4 * g + 1), c),
+                   code_of<T>(Elem<T>::at(u, 4 * g + 2), c), code_of<T>(Elem<T>::at(u, 4 * g + 3), c));
   }
   if (!TAIL || col + PER <= K) {
     if (PER == 8) *reinterpret_cast<uint2*>(qc) = make_uint2(w[0], w[PER / 4 - 1]);
@@ -188,18 +188,18 @@ __device__ __noinline__ uint4 load_chunk_edge(const T* xr, int col, int K) {
 
 // Rows of any alignment: the aligned 16-byte units that a row lies in come to shared memory
 // by asynchronous copies, and a chunk is put together from two of them.  Other bytes of the
-// first and last unit belong to the neighbouring rows; the first row's first unit and the
-// last row's last one, which may have no neighbour, are read within the matrix only.
+// first and last unit belong to neighbouring rows or the gap between them; of a unit that
+// reaches past the matrix (x .. end) only the bytes within it are read.
 __device__ __forceinline__ uint32_t row_off(const void* xr) { return (uint32_t)reinterpret_cast<uintptr_t>(xr) & 15u; }
 
 // Unit i of a row to dst.  off: bytes of unit 0 before the row.
 template <class T>
-__device__ __forceinline__ void fetch_unit(const T* xr, uint32_t off, int i, int K, bool first_row, bool last_row,
+__device__ __forceinline__ void fetch_unit(const T* xr, uint32_t off, int i, int K, const T* x, const T* end,
                                            uint4* dst) {
   constexpr int PER = Elem<T>::PER;
   const char* from = reinterpret_cast<const char*>(xr) - off + (size_t)i * 16;
-  const int left = K * (int)sizeof(T) + (int)off - i * 16;   // bytes up to the end of the row
-  if (i == 0 && off && first_row) {
+  const long long left = reinterpret_cast<const char*>(end) - from;
+  if (from < reinterpret_cast<const char*>(x)) {
     const int lead = (int)(off / sizeof(T));
     uint4 u = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
@@ -211,7 +211,7 @@ __device__ __forceinline__ void fetch_unit(const T* xr, uint32_t off, int i, int
     }
     *dst = u;
   } else {
-    cp_async16(smem_u32(dst), from, last_row && left < 16 ? (uint32_t)left : 16u);
+    cp_async16(smem_u32(dst), from, left < 16 ? (uint32_t)left : 16u);
   }
 }
 // The chunk at column col from its units a and b (off as above), zeros past K.
@@ -283,7 +283,9 @@ __device__ __forceinline__ uint32_t gelu_bits(uint32_t x) { return g_gelu_table[
 // The magnitudes 2^-14 .. 16 of the GELU table as shared-memory words: GELU(x) and
 // GELU(-x) in the low and high half of word bits(x) - kGeluLo (9 KB; lanes that differ
 // only in sign read one word).  Chunks with another value (zeros, infinities, about 1 in
-// 800 of a unit normal's) take the whole table from global memory.
+// 800 of a unit normal's) take the whole table from global memory.  25024 x 4304: 73.9 us,
+// the HBM floor being 49.4; the table reads bound it (shared memory busy 83 % of the time,
+// bank conflicts among random words included, issue slots 61 %).
 constexpr uint32_t kGeluLo = 0x3880u, kGeluN = 0x900u;
 
 __device__ __forceinline__ void gelu_stage(uint32_t* lut) {
@@ -329,7 +331,9 @@ __device__ __forceinline__ uint4 gelu_chunk(const uint4& u, const uint32_t* lut)
 // once.  ANY: rows of any alignment and K, by way of shared memory (`units` 16-byte units a
 // row; the next row's are on their way while this one's codes are stored); otherwise whole
 // 16-byte chunks.  Plain rows: one CTA for each (or 8 rows, a warp each); GELU: persistent
-// over the rows, since every CTA stages the table.
+// over the rows, since every CTA stages the table.  Bound by memory: 9164 x 1152 bf16
+// 4.85 us (floor 4.8; 32 MB, which stay in L2 between calls), 4608 x 4608 fp32 19.5 (16.2);
+// rows of 1153, which start anywhere, 10.9.
 template <int OP, class T, int TPR, int NC, bool ANY>
 __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR)
     rows_int8_kernel(const T* x, int ldx, int M, int K, int units, int8_t* q, int ldq,
@@ -351,7 +355,7 @@ __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR)
     const T* xr = x + (size_t)row * ldx;
     const uint32_t off = row_off(xr);
     const int n = (K * (int)sizeof(T) + (int)off + 15) / 16;
-    for (int i = t; i < n; i += TPR) fetch_unit(xr, off, i, K, row == 0, row == M - 1, mine + i);
+    for (int i = t; i < n; i += TPR) fetch_unit(xr, off, i, K, x, x + (size_t)(M - 1) * ldx + K, mine + i);
     cp_async_commit();
   };
   // whole warps (TPR = 32) or whole CTAs share a row
@@ -399,10 +403,13 @@ __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR)
 // TPR threads per row: half a warp, a warp, or a CTA of 128.  A thread's chunks (8 columns
 // each) go to shared memory by 16-byte asynchronous copies and stay there, private to the
 // thread, through the three passes over them (statistics, normalised bf16 values in place,
-// codes): the loops stay rolled and the registers few, so that 32 warps share an SM and
-// hide each other's latencies.  (Held in registers, 36 a thread, the same arithmetic ran
-// 20 warps an SM, missed the instruction cache and took 33.6 us against 25024 x 1152.)
-// gamma and beta are staged once per CTA as fp32; persistent over the rows.
+// codes): the loops stay rolled and the registers few, so that 32 warps share an SM and hide
+// each other's latencies, and one kernel takes any width and alignment.  (25024 x 1152:
+// 34.3 us, 25024 x 1153: 46.5, 6256 x 4608: 46.4.  With the row held in registers, 36 a
+// thread and 20 warps an SM, 1152 columns took 33.6, but that kernel held no wider or
+// unaligned row.)  gamma and beta are staged once per CTA as fp32; persistent over the rows.
+// Bound by issue slots (69 % busy), not by HBM (floor 13.2 us): about 25 instructions an
+// element, of which the bracket below costs 4 us, the codes 5 and the fp64 statistics 1.5.
 //
 // Statistics: exact fp64 sums of x and x^2 (bf16 -> fp64 is exact); where the mean is
 // far above the spread (E[x^2] > 2^10 var), which would cost the difference its bits,
@@ -469,7 +476,8 @@ __global__ void __launch_bounds__(TPR == 128 ? 128 : kLn8Threads, TPR == 128 ? 8
     if constexpr (ANY) {   // the row's units; unit i has the place of chunk i
       const uint32_t off = row_off(xt - t * 8);
       const int n = (K * 2 + (int)off + 15) / 16;
-      for (int c = 0, i = t; i < n; ++c, i += TPR) fetch_unit(xt - t * 8, off, i, K, r == 0, r == M - 1, mine + c * pitch);
+      const __nv_bfloat16* end = x + (size_t)(M - 1) * ldx + K;
+      for (int c = 0, i = t; i < n; ++c, i += TPR) fetch_unit(xt - t * 8, off, i, K, x, end, mine + c * pitch);
     } else {
       uint32_t dst = mine_s;
 #pragma unroll 3
@@ -588,7 +596,7 @@ __global__ void __launch_bounds__(TPR == 128 ? 128 : kLn8Threads, TPR == 128 ? 8
         const uint64_t e = f2pack(fabsf(yf.x) + fabsf(b[2 * i]), fabsf(yf.y) + fabsf(b[2 * i + 1]));
         h[i] = bf16x2_of(ffma2(e, dn, y));
         differ |= h[i] ^ bf16x2_of(ffma2(e, up, y));
-        cm = fmax3(cm, fabsf(yf.x), fabsf(yf.y));
+        cm = fmax3_nan(cm, fabsf(yf.x), fabsf(yf.y));   // gamma or beta may bring a NaN
       }
       uint4 w = make_uint4(h[0], h[1], h[2], h[3]);
       if (differ) {

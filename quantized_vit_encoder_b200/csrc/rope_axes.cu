@@ -122,8 +122,9 @@ __global__ void __launch_bounds__(VEC == 1 ? 2 * kRopeAxThreads : kRopeAxThreads
 }
 
 // Tokens of a CTA: about as many angles as make it worth the wait, as few as keep its
-// accesses together (heads of 128, 2 tokens: 54.0 us for 336 MB, 4: 55.8, 8: 60.5; of 72, 4:
-// 19.7 us for 76 MB in the first kernel, 2: 20.6), and fewer where that leaves SMs idle.
+// accesses together (16384 tokens of 40 heads of 128: 2 tokens 55.2 us, 3 56.8, 5 61.6, 8 64.8;
+// 8192 of 32 heads of 72: 3 19.9, 4 19.7, 5 20.6, 8 20.5), and fewer where that leaves SMs
+// idle.
 int rope_tokens(const RopeAxes& p, int num_sms) {
   int toks = 144 / p.pairs;
   if (toks > p.n / (4 * num_sms)) toks = p.n / (4 * num_sms);

@@ -153,6 +153,21 @@ def test_widest_rows(K):
     _same(vitq.gelu_quant_int8(x), _codes_ref(_gelu_ref(x)), K)
 
 
+@pytest.mark.parametrize("K", [40, 1152, 1153, 2056, 4608, 16392])
+def test_ln_quant_not_finite_gamma_or_beta(K):
+    """A NaN that only gamma or beta brings in (or 0 * infinity) marks every row it reaches."""
+    x = _randn(3, 5, K).to(BF)
+    x[3] = 1.25                                     # x - mean = 0
+    one, zero = torch.ones(K, dtype=BF, device="cuda"), torch.zeros(K, dtype=BF, device="cuda")
+    for col in (0, K // 2, K - 1):
+        for v in (float("nan"), float("inf"), -float("inf")):
+            for w in (one, zero):
+                bad = w.clone()
+                bad[col] = v
+                q, s = vitq.ln_quant_int8(x, *((bad, zero) if w is one else (one, bad)))
+                assert torch.isnan(s).all() and (q == 0).all(), (col, v, w is one)
+
+
 def test_ln_quant_unaligned_gamma_and_beta():
     K = 1152
     x = _randn(1, 50, K).to(BF)
