@@ -242,7 +242,8 @@ size_t vitq_patch_embed_workspace_bytes(int n_tokens);
 
 /* Element types of the entry points below that take one.  With no rows (M or
  * n_tokens 0) these entry points return VITQ_OK and launch nothing, and the pointers
- * of the row matrices may be NULL. */
+ * of the row matrices may be NULL.  An output shares no memory with an input or
+ * another output, except where its entry point says so. */
 #define VITQ_BF16 0
 #define VITQ_FP16 1
 #define VITQ_FP32 2

@@ -66,6 +66,7 @@ int int8_gemm(const int8_t* A, int lda, const float* sA, const int8_t* W, int ld
   VITQ_CHECK(W && sW && dtype_ok(dtype) && (M == 0 || (A && sA && C)), VITQ_ERR_INVALID_ARG);
   VITQ_CHECK(M >= 0 && N > 0 && K > 0 && lda >= K && ldw >= K && ldc >= N && (!residual || ldr >= N),
              VITQ_ERR_INVALID_ARG);
+  VITQ_CHECK(!residual || residual != C || ldr == ldc || M <= 1, VITQ_ERR_INVALID_ARG);
   VITQ_CHECK(M <= VITQ_MAX_ROWS && N <= VITQ_MAX_DIM && K <= VITQ_MAX_DIM, VITQ_ERR_SHAPE);
   VITQ_CHECK(lda % 16 == 0 && ldw % 16 == 0, VITQ_ERR_SHAPE);
   const int es = elem_bytes(dtype);

@@ -371,6 +371,9 @@ _BF16_ONLY, _I8_ONLY, _F32_ONLY = (_bf16,), (torch.int8,), (_f32,)
 # tensor once; a call that fails a check is explained by _why.
 
 
+_INT_MAX = (1 << 31) - 1   # sizes and row strides pass the C ABI as int32
+
+
 def _device(t, name):
     """Index of the current device, where the library launches and every tensor has to live (t: the first of them)."""
     if _DEVICE_TYPE != "cuda":
@@ -399,6 +402,8 @@ def _why(t, name, dev, dtypes, shape, dense):
         return VitqError(f"{name}: dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
     if t.dim() != len(shape) or any(w is not None and w != d for w, d in zip(shape, t.shape)):
         return VitqError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if max(*t.shape, *t.stride()) > _INT_MAX:
+        return VitqError(f"{name}: shape {tuple(t.shape)}, strides {t.stride()}: sizes past 2^31 - 1")
     return VitqError(f"{name}: strides {t.stride()}, expected {dense}")
 
 
@@ -412,7 +417,7 @@ def _mat(t, name, dev, dtypes, rows=None, cols=None):
     ld, inner = t.stride()
     if m <= 1:
         ld = (k + 15) // 16 * 16
-    if (inner != 1 and k > 1) or ld < k:
+    if (inner != 1 and k > 1) or ld < k or ld > _INT_MAX or m > _INT_MAX:
         raise _why(t, name, dev, dtypes, (rows, cols), "dense rows")
     return m, k, ld
 
@@ -514,7 +519,8 @@ def _heads(t, name, dev, dtypes, n=None, h=None, d=None):
         raise _why(t, name, dev, dtypes, (n, h, d), "")
     tn, th, td = t.shape
     st, sh, sd = t.stride()
-    if (n is not None and tn != n) or (h is not None and th != h) or (d is not None and td != d) or (sd != 1 and td > 1):
+    if ((n is not None and tn != n) or (h is not None and th != h) or (d is not None and td != d) or
+            (sd != 1 and td > 1) or max(tn, th, td) > _INT_MAX):
         raise _why(t, name, dev, dtypes, (n, h, d), "a dense innermost dimension")
     return tn, th, td, st, sh
 

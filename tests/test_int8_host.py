@@ -67,7 +67,8 @@ GEMM = dict(A=P, lda=64, sA=P, W=P, ldw=64, sW=P, bias=None, res=None, ldr=0, C=
     (dict(lda=72), SHAPE), (dict(ldw=72), SHAPE), (dict(M=(1 << 24) + 1), SHAPE), (dict(M=(1 << 31) - 1), SHAPE),
     (dict(N=(1 << 16) + 8, ldc=1 << 17), SHAPE), (dict(K=(1 << 16) + 16, lda=1 << 17, ldw=1 << 17), SHAPE),
     (dict(A=V(4104)), ALIGN), (dict(W=V(4104)), ALIGN), (dict(C=V(4097)), ALIGN), (dict(C=V(4098), dtype=2), ALIGN),
-    (dict(bias=V(4097)), ALIGN), (dict(res=V(4097), ldr=40), ALIGN), (dict(sA=V(4098)), ALIGN)])
+    (dict(bias=V(4097)), ALIGN), (dict(res=V(4097), ldr=40), ALIGN), (dict(sA=V(4098)), ALIGN),
+    (dict(res=P, ldr=48), INVALID)])                # the residual in place, but with another row stride than C's
 def test_int8_gemm_refusals(lib, bad, code):
     a = GEMM | bad
     assert lib.int8_gemm(*[a[k] for k in GEMM], None) == code
@@ -227,6 +228,26 @@ def test_binding_marshals_rope(on_cpu):
 def test_binding_refusals(on_cpu, call):
     with pytest.raises(vitq.VitqError):
         call()
+    assert not on_cpu.calls
+
+
+def test_binding_refuses_sizes_past_int32(on_cpu, monkeypatch):
+    """Sizes and strides that would wrap around in a C int (meta tensors: no memory behind them)."""
+    monkeypatch.setattr(vitq, "_DEVICE_TYPE", "meta")
+    big = 1 << 31
+
+    def meta(shape, strides, t=torch.bfloat16):
+        return torch.empty_strided(shape, strides, dtype=t, device="meta")
+    for call in (lambda: vitq.quant_int8(meta((2, 32), (big + 32, 1))),
+                 lambda: vitq.quant_int8(meta((2 * big + 4, 32), (32, 1))),
+                 lambda: vitq.gelu_quant_int8(meta((2, 32), (2 * big + 32, 1))),
+                 lambda: vitq.int8_gemm(meta((4, 32), (big + 32, 1), torch.int8), torch.zeros(4), _i8(8, 32), torch.zeros(8)),
+                 lambda: vitq.int8_gemm(_i8(4, 32), torch.zeros(4), _i8(8, 32), torch.zeros(8),
+                                        out=meta((4, 8), (2 * big + 8, 1))),
+                 lambda: vitq.rope_axes(meta((2 * big + 4, 2, 8), (16, 8, 1)), None,
+                                        meta((2 * big + 4, 1), (1, 1), torch.int32), (4,))):
+        with pytest.raises(vitq.VitqError, match="2\\^31"):
+            call()
     assert not on_cpu.calls
 
 
