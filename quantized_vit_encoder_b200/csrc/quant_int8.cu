@@ -283,9 +283,9 @@ __device__ __forceinline__ uint32_t gelu_bits(uint32_t x) { return g_gelu_table[
 // The magnitudes 2^-14 .. 16 of the GELU table as shared-memory words: GELU(x) and
 // GELU(-x) in the low and high half of word bits(x) - kGeluLo (9 KB; lanes that differ
 // only in sign read one word).  Chunks with another value (zeros, infinities, about 1 in
-// 800 of a unit normal's) take the whole table from global memory.  25024 x 4304: 73.9 us,
-// the HBM floor being 49.4; the table reads bound it (shared memory busy 83 % of the time,
-// bank conflicts among random words included, issue slots 61 %).
+// 800 of a unit normal's) take the whole table from global memory.  25024 x 4304: 70.1 us,
+// the HBM floor being 49.4; the table reads bound it (3.4 words of one bank among 32 random
+// ones: before rows were loaded ahead, shared memory was busy 83 % of 74 us, issue slots 61 %).
 constexpr uint32_t kGeluLo = 0x3880u, kGeluN = 0x900u;
 
 __device__ __forceinline__ void gelu_stage(uint32_t* lut) {
@@ -333,9 +333,20 @@ __device__ __forceinline__ uint4 gelu_chunk(const uint4& u, const uint32_t* lut)
 // 16-byte chunks.  Plain rows: one CTA for each (or 8 rows, a warp each); GELU: persistent
 // over the rows, since every CTA stages the table.  Bound by memory: 9164 x 1152 bf16
 // 4.85 us (floor 4.8; 32 MB, which stay in L2 between calls), 4608 x 4608 fp32 19.5 (16.2);
-// rows of 1153, which start anywhere, 10.9.
+// rows of 1153, which start anywhere, 10.9.  Rows
+// of any alignment by 28 warps an SM in fp32 (9164 x 1153: 31.7 us, by the 20 that the
+// compiler's registers leave 36.6); in 2 bytes that many spill.
+// Whole GELU chunks (kAhead): the next row is on its way, in registers, while this one is
+// worked on, at 16 warps an SM (25024 x 4304: 70.1 us, 972 x 4304: 5.0; without it 28 warps
+// 73.8 and 7.6, 20 warps 73.2 and 5.9; with it by way of shared memory 20 warps 69.4 and 6.1).
+template <int OP, int TPR, bool ANY> constexpr bool kAhead = OP == kI8Gelu && !ANY && TPR < 1024;
+// CTAs an SM that the registers leave room for; 0: as the compiler sees fit.
+template <int OP, class T, int TPR, bool ANY>
+constexpr int kRowCtas = kAhead<OP, TPR, ANY> ? (TPR == 32 ? 2 : 512 / TPR)
+                         : ANY && sizeof(T) == 4 && TPR < 1024 ? (TPR == 32 ? 3 : 896 / TPR) : 0;
+
 template <int OP, class T, int TPR, int NC, bool ANY>
-__global__ void __launch_bounds__(TPR == 32 ? 256 : TPR)
+__global__ void __launch_bounds__(TPR == 32 ? 256 : TPR, kRowCtas<OP, T, TPR, ANY>)
     rows_int8_kernel(const T* x, int ldx, int M, int K, int units, int8_t* q, int ldq,
                      float* s) {
   constexpr int PER = Elem<T>::PER;
@@ -361,25 +372,33 @@ __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR)
   // whole warps (TPR = 32) or whole CTAs share a row
   int row = blockIdx.x * ROWS + (TPR == 32 ? threadIdx.x >> 5 : 0);
   if (ANY && row < M) fetch(row);
+  uint4 u[NC], next[kAhead<OP, TPR, ANY> ? NC : 1];   // chunks of this row, and of the next
+  auto load = [&](int r, uint4* to) {
+    const T* xt = x + (size_t)r * ldx + t * PER;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      to[c] = make_uint4(0u, 0u, 0u, 0u);
+      if ((c * TPR + t) * PER < K) to[c] = *reinterpret_cast<const uint4*>(xt + c * TPR * PER);
+    }
+  };
+  if (kAhead<OP, TPR, ANY> && row < M) load(row, next);
   for (; row < M; row += gridDim.x * ROWS) {
-    const T* xt = x + (size_t)row * ldx + t * PER;
-    uint4 u[NC];
     if (ANY) {
       cp_async_wait<0>();
       if (TPR == 32) __syncwarp();
       else __syncthreads();
-      const uint32_t off = row_off(xt - t * PER);
+      const uint32_t off = row_off(x + (size_t)row * ldx);
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
         const int i = c * TPR + t, col = i * PER;
         u[c] = col < K ? chunk_of_units<T>(mine[i], mine[i + 1], off, col, K) : make_uint4(0u, 0u, 0u, 0u);
       }
-    } else {
+    } else if (kAhead<OP, TPR, ANY>) {
 #pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        u[c] = make_uint4(0u, 0u, 0u, 0u);
-        if ((c * TPR + t) * PER < K) u[c] = *reinterpret_cast<const uint4*>(xt + c * TPR * PER);
-      }
+      for (int c = 0; c < NC; ++c) u[c] = next[c % (int)(sizeof(next) / sizeof(uint4))];
+      if (row + (int)gridDim.x * ROWS < M) load(row + gridDim.x * ROWS, next);
+    } else {
+      load(row, u);
     }
     uint32_t m = 0u;
 #pragma unroll
@@ -693,11 +712,11 @@ bool rows_whole(const RowsInt8& a) {
 template <int OP, class T, int TPR, int NC>
 cudaError_t rows_launch(const RowsInt8& a, int num_sms, cudaStream_t st) {
   long long grid = TPR == 32 ? ((long long)a.M + 7) / 8 : a.M;
-  if (OP == kI8Gelu) {   // as many CTAs as fit the GPU (about 28 warps an SM)
-    const long long most = (long long)num_sms * (TPR == 32 ? 3 : TPR >= 1024 ? 1 : 896 / TPR);
+  const bool whole = rows_whole<T>(a);
+  if (OP == kI8Gelu) {   // as many CTAs as fit the GPU (16 warps an SM; rows of any alignment: as many)
+    const long long most = (long long)num_sms * (TPR == 32 ? 2 : TPR >= 1024 ? 1 : 512 / TPR);
     if (grid > most) grid = most;
   }
-  const bool whole = rows_whole<T>(a);
   auto kern = whole ? rows_int8_kernel<OP, T, TPR, NC, false> : rows_int8_kernel<OP, T, TPR, NC, true>;
   const int units = (a.K * (int)sizeof(T) + 15) / 16 + 2;   // a row in units it may not start on, and one behind
   const size_t smem = whole ? 0 : (size_t)units * 16 * (TPR == 32 ? 8 : 1);

@@ -3,7 +3,8 @@
     python -m quantized_vit_encoder_b200.profile_case STAGE [--iters N]
 
 STAGE: attention | gemm_qkv | gemm_proj | gemm_fc1 | gemm_fc2 | bf16_qkv | bf16_proj | bf16_fc1 |
-       bf16_fc2 | ln_quant | ln_quant_merger | quant_act | gelu_quant | rope | block | tower.
+       bf16_fc2 | ln_quant | ln_quant_merger | quant_act | gelu_quant | rope | block | tower |
+       int8_qkv | int8_proj | int8_fc1 | int8_fc2 | quant_int8 | ln_quant_int8 | gelu_quant_int8 | rope_axes.
 Device memory stays below 0.5 GB except for tower (the 27 blocks' and 4 mergers'
 weights, about 1 GB); each iteration is one launch of the stage's kernel (block:
 the ten launches of one block; tower: the 288 launches of one tower pass).  The
@@ -77,6 +78,24 @@ def main():
     elif a.stage == "gelu_quant":
         f = wl.random_bf16((n, 4304), 4, 1.0).to(dev)
         run = lambda: vitq.gelu_quant(f)  # noqa: E731
+    elif a.stage.startswith("int8_"):
+        name = a.stage[5:]
+        w = t[name + "_w"]
+        qa, sa = vitq.quant_int8(wl.random_bf16((n, w.shape[1]), 2, 1.0).to(dev))
+        qw, sw = vitq.quant_int8(w)
+        res = x if name == "proj" else (wl.random_bf16((n, 1152), 3).to(dev) if name == "fc2" else None)
+        run = lambda: vitq.int8_gemm(qa, sa, qw, sw, t[name + "_b"], res)  # noqa: E731
+    elif a.stage == "quant_int8":
+        run = lambda: vitq.quant_int8(x)  # noqa: E731
+    elif a.stage == "ln_quant_int8":
+        run = lambda: vitq.ln_quant_int8(x, t["norm1_w"], t["norm1_b"])  # noqa: E731
+    elif a.stage == "gelu_quant_int8":
+        f = wl.random_bf16((n, 4304), 4, 1.0).to(dev)
+        run = lambda: vitq.gelu_quant_int8(f)  # noqa: E731
+    elif a.stage == "rope_axes":
+        qkv = wl.random_bf16((n, 3456), 5, 1.0).to(dev)
+        q, k = qkv[:, :1152].view(n, 16, 72), qkv[:, 1152:2304].view(n, 16, 72)
+        run = lambda: vitq.rope_axes(q, k, pos, (18, 18), axis_freq=True)  # noqa: E731
     elif a.stage == "rope":
         qkv = wl.random_bf16((n, 3456), 5, 1.0).to(dev)
         run = lambda: vitq.rope2d_(qkv, cs)  # noqa: E731
