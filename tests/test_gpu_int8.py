@@ -497,3 +497,55 @@ def test_two_streams_at_once():
                 got[i] = _chain(xs[i], p)
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+# ------------------------------------------------------------------ more rows than run at once, far offsets
+@pytest.mark.parametrize("M,K", [(5000, 1152), (5001, 1001), (5003, 2304), (3000, 4304), (2501, 4303), (1300, 9000), (1301, 9001),
+                                 (700, 18000), (701, 17999), (400, 24000), (401, 24001)])
+def test_gelu_quant_more_rows_than_run_at_once(M, K):
+    f = (_randn(M, M, K) * torch.exp(_randn(K, M, 1))).to(BF)
+    _same(vitq.gelu_quant_int8(f), _codes_ref(_gelu_ref(f)), (M, K))
+
+
+@pytest.mark.parametrize("M,K", [(20001, 1152), (10001, 264), (10003, 1151), (5000, 2000), (5003, 2001), (1500, 4608),
+                                 (1503, 4607), (450, 16000), (451, 15999)])
+def test_ln_quant_more_rows_than_run_at_once(M, K):
+    x = (_randn(M, M, K) * torch.exp(_randn(K, M, 1)) + _randn(M + 1, M, 1)).to(BF)
+    gamma, beta = (1 + 0.1 * _randn(1, K)).to(BF), (0.1 * _randn(2, K)).to(BF)
+    _same(vitq.ln_quant_int8(x, gamma, beta), _codes_ref(_ln_ref(x, gamma, beta, 1e-6)), (M, K))
+
+
+FAR_ROWS, FAR_STRIDE = 33001, 65536 + 16        # 2.16e9 elements from the first row to the last
+
+
+@pytest.mark.parametrize("pad", [0, 1])
+@pytest.mark.parametrize("fn", ["quant", "ln", "gelu"])
+def test_rows_past_32_bit_offsets(fn, pad):
+    """Rows of x and of the codes more than 2^31 elements apart (4.3 and 2.2 GB); pad: a stride of any alignment."""
+    ld, K = FAR_STRIDE + pad, 72
+    x = torch.empty(FAR_ROWS * ld, dtype=BF, device="cuda").as_strided((FAR_ROWS, K), (ld, 1))
+    x.copy_(_randn(3, FAR_ROWS, K))
+    out = (torch.empty(FAR_ROWS * FAR_STRIDE, dtype=torch.int8, device="cuda").as_strided((FAR_ROWS, K), (FAR_STRIDE, 1)),
+           torch.empty(FAR_ROWS, device="cuda"))
+    w = torch.ones(K, dtype=BF, device="cuda")
+    call = {"quant": vitq.quant_int8, "gelu": vitq.gelu_quant_int8,
+            "ln": lambda a, out=None: vitq.ln_quant_int8(a, w, w, out=out)}[fn]
+    want = call(x.contiguous())
+    got = call(x, out=out)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("pad", [0, 3])
+@pytest.mark.parametrize("N,K", [(40, 200), (264, 640)])
+def test_gemm_past_32_bit_offsets(N, K, pad):
+    """A, the residual and C with rows more than 2^31 elements apart (2.2, 4.3 and 4.3 GB)."""
+    M, ld = FAR_ROWS, FAR_STRIDE + pad
+    far = torch.empty(M * FAR_STRIDE, dtype=torch.int8, device="cuda").as_strided((M, K), (FAR_STRIDE, 1))
+    qa, qw = _i8(1, M, K), _i8(2, N, K)
+    far.copy_(qa)
+    sa, sw = torch.rand(M, device="cuda"), torch.rand(N, device="cuda")
+    r, c = (torch.empty(M * ld, dtype=BF, device="cuda").as_strided((M, N), (ld, 1)) for _ in range(2))
+    r.copy_(_randn(4, M, N))
+    want = vitq.int8_gemm(qa, sa, qw, sw, residual=r.contiguous())
+    assert torch.equal(vitq.int8_gemm(far, sa, qw, sw, residual=r, out=c), want)
+    assert vitq.device_error() == 0
