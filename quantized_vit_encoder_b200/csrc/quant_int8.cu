@@ -338,8 +338,9 @@ __device__ __forceinline__ uint4 gelu_chunk(const uint4& u, const uint32_t* lut)
 // compiler's registers leave 36.6); in 2 bytes that many spill.
 // Whole GELU chunks (kAhead): the next row is on its way, in registers, while this one is
 // worked on, at 16 warps an SM (25024 x 4304: 70.1 us, 972 x 4304: 5.0; without it 28 warps
-// 73.8 and 7.6, 20 warps 73.2 and 5.9; with it by way of shared memory 20 warps 69.4 and 6.1).
-template <int OP, int TPR, bool ANY> constexpr bool kAhead = OP == kI8Gelu && !ANY && TPR < 1024;
+// 73.8 and 7.6, 20 warps 73.2 and 5.9; with it by way of shared memory 20 warps 69.4 and 6.1; 256 threads a
+// row, 3128 x 18000: 42.1 with it, 40.1 without).
+template <int OP, int TPR, bool ANY> constexpr bool kAhead = OP == kI8Gelu && !ANY && TPR <= 128;
 // CTAs an SM that the registers leave room for; 0: as the compiler sees fit.
 template <int OP, class T, int TPR, bool ANY>
 constexpr int kRowCtas = kAhead<OP, TPR, ANY> ? (TPR == 32 ? 2 : 512 / TPR)
@@ -713,8 +714,8 @@ template <int OP, class T, int TPR, int NC>
 cudaError_t rows_launch(const RowsInt8& a, int num_sms, cudaStream_t st) {
   long long grid = TPR == 32 ? ((long long)a.M + 7) / 8 : a.M;
   const bool whole = rows_whole<T>(a);
-  if (OP == kI8Gelu) {   // as many CTAs as fit the GPU (16 warps an SM; rows of any alignment: as many)
-    const long long most = (long long)num_sms * (TPR == 32 ? 2 : TPR >= 1024 ? 1 : 512 / TPR);
+  if (OP == kI8Gelu) {   // as many CTAs as fit the GPU: 16 warps an SM, 256 threads a whole row 24
+    const long long most = (long long)num_sms * (TPR == 32 ? 2 : TPR >= 1024 ? 1 : TPR == 256 && whole ? 3 : 512 / TPR);
     if (grid > most) grid = most;
   }
   auto kern = whole ? rows_int8_kernel<OP, T, TPR, NC, false> : rows_int8_kernel<OP, T, TPR, NC, true>;
