@@ -722,7 +722,10 @@ cudaError_t rows_launch(const RowsInt8& a, int num_sms, cudaStream_t st) {
   const int units = (a.K * (int)sizeof(T) + 15) / 16 + 2;   // a row in units it may not start on, and one behind
   const size_t smem = whole ? 0 : (size_t)units * 16 * (TPR == 32 ? 8 : 1);
   if (smem > 32 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // The limit is the kernel's, not the launch's: always the most that any row takes, so that a call in another
+    // thread does not lower it between this and the launch.
+    constexpr int kMost = (NC * TPR + 2) * 16 * (TPR == 32 ? 8 : 1);
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
     if (e != cudaSuccess) return e;
   }
   return launch_pdl(kern, dim3((unsigned)grid), dim3(TPR == 32 ? 256 : TPR), smem, st, (const T*)a.x, a.ldx, a.M, a.K,
@@ -735,16 +738,22 @@ cudaError_t rows_any_launch(const RowsInt8& a, cudaStream_t st) {
                     a.M, a.K, a.gamma, a.beta, a.eps, a.q, a.ldq, a.s);
 }
 
+// Chunks a thread at most (launch_ln_quant_int8 goes by it).
+template <int TPR> constexpr int kLn8Chunks = TPR == 16 ? 9 : TPR == 32 ? 8 : 16;
+
 template <int TPR>
 cudaError_t ln_rows_launch(const RowsInt8& a, int num_sms, cudaStream_t st) {
   const int nc = (a.K + 8 * TPR - 1) / (8 * TPR);
+  constexpr int kMostThreads = TPR == 128 ? 128 : kLn8Threads;
   // as many threads a CTA as leave every SM one (gamma and beta are staged once a CTA)
-  int threads = TPR == 128 ? 128 : kLn8Threads;
+  int threads = kMostThreads;
   while (threads > 32 && TPR < 128 && (long long)num_sms * threads / TPR > a.M) threads /= 2;
   // (one more row of chunks for the unit behind the last in rows that start inside one)
   const size_t smem = (size_t)nc * 16 * (4 * TPR + threads) + (rows_whole<__nv_bfloat16>(a) ? 0 : 16 * threads);
   auto kern = rows_whole<__nv_bfloat16>(a) ? ln_rows_int8_kernel<TPR, false> : ln_rows_int8_kernel<TPR, true>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  // the kernel's limit, as in rows_launch: the most that any row and number of rows takes
+  constexpr int kMost = kLn8Chunks<TPR> * 16 * (4 * TPR + kMostThreads) + 16 * kMostThreads;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
   if (e != cudaSuccess) return e;
   const int per_sm = (int)(220 * 1024 / (smem + 1024));
   const int rows = threads / TPR;
@@ -779,9 +788,9 @@ cudaError_t launch_quant_int8(const RowsInt8& a, int dtype, int num_sms, cudaStr
 cudaError_t launch_ln_quant_int8(const RowsInt8& a, int num_sms, cudaStream_t st) {
   if (a.M == 0) return cudaSuccess;
   const int chunks = (a.K + 7) / 8;
-  if (chunks <= 144) return ln_rows_launch<16>(a, num_sms, st);
-  if (chunks <= 256) return ln_rows_launch<32>(a, num_sms, st);
-  if (chunks <= 2048) return ln_rows_launch<128>(a, num_sms, st);
+  if (chunks <= 16 * kLn8Chunks<16>) return ln_rows_launch<16>(a, num_sms, st);
+  if (chunks <= 32 * kLn8Chunks<32>) return ln_rows_launch<32>(a, num_sms, st);
+  if (chunks <= 128 * kLn8Chunks<128>) return ln_rows_launch<128>(a, num_sms, st);
   return rows_any_launch<kI8Ln, __nv_bfloat16>(a, st);
 }
 cudaError_t launch_gelu_quant_int8(const RowsInt8& a, int num_sms, cudaStream_t st) {

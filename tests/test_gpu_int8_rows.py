@@ -1,0 +1,137 @@
+"""The INT8 row kernels where a call is hard on them: calls from two host threads, LayerNorm rows without
+spread, statistics and results at the ends of the number range.
+
+Codes and scales are compared bit for bit with the definition in 64 bits, stated directly where the
+definition is plain (a constant row's LayerNorm is beta).
+"""
+import ctypes as C
+import math
+import os
+import shutil
+import subprocess
+
+import pytest
+import torch
+
+from quantized_vit_encoder_b200 import vitq
+
+pytestmark = pytest.mark.gpu
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+BF, HF, F32 = torch.bfloat16, torch.float16, torch.float32
+
+
+def _randn(seed, *shape):
+    return torch.randn(shape, generator=torch.Generator(device="cuda").manual_seed(seed), device="cuda")
+
+
+def _codes_ref(y):
+    """(codes, scales) of rows of y, from the definition."""
+    amax = y.abs().amax(1).float()
+    s = torch.where(torch.isfinite(amax), amax / torch.full_like(amax, 127), math.nan)   # a division, not a product
+    q = torch.round(y.double() / s.double()[:, None])
+    return torch.where((s > 0)[:, None], q, 0.0).clamp(-127, 127).to(torch.int8), s
+
+
+def _same(got, want, what=""):
+    q, s = got
+    torch.cuda.synchronize()
+    wq, ws = want
+    assert torch.equal(s.nan_to_num(-1.0), ws.nan_to_num(-1.0)), f"{what}: scales differ"
+    bad = (q != wq).nonzero()
+    assert not len(bad), f"{what}: {len(bad)} codes differ, first at {bad[:3].tolist()}"
+    assert vitq.device_error() == 0
+
+
+# ------------------------------------------------------------------ calls from two host threads
+HAMMER = r"""
+#include <pthread.h>
+#include "vitq.h"
+typedef struct {
+  int kind, dtype, M, K, ldx, ldq, n, failed, status;
+  const void *x, *gamma, *beta;
+  int8_t* q;
+  float* s;
+  void* stream;
+  pthread_barrier_t* start;
+} job;
+static void* work(void* p) {
+  job* j = (job*)p;
+  pthread_barrier_wait(j->start);
+  for (int i = 0; i < j->n; ++i) {
+    int r = j->kind == 0   ? vit_quant_int8(j->x, j->dtype, j->M, j->K, j->ldx, j->q, j->ldq, j->s, j->stream)
+            : j->kind == 1 ? vit_ln_quant_int8(j->x, j->M, j->K, j->ldx, j->gamma, j->beta, 1e-6f, j->q, j->ldq, j->s, j->stream)
+            : j->kind == 2 ? vit_gelu_quant_int8(j->x, j->M, j->K, j->ldx, j->q, j->ldq, j->s, j->stream)
+                           : vit_ln_quant(j->x, j->M, j->K, j->ldx, j->gamma, j->beta, 1e-6f, (uint8_t*)j->q, j->s, j->ldq, j->stream);
+    if (r) j->failed++, j->status = r;
+  }
+  return 0;
+}
+int hammer(job* jobs, int threads) {
+  pthread_barrier_t start;
+  pthread_t t[8];
+  int failed = 0;
+  pthread_barrier_init(&start, 0, (unsigned)threads);
+  for (int i = 0; i < threads; ++i) jobs[i].start = &start;
+  for (int i = 0; i < threads; ++i) pthread_create(&t[i], 0, work, &jobs[i]);
+  for (int i = 0; i < threads; ++i) {
+    pthread_join(t[i], 0);
+    failed += jobs[i].failed;
+  }
+  pthread_barrier_destroy(&start);
+  return failed;
+}
+"""
+
+
+class Job(C.Structure):
+    _fields_ = ([(n, C.c_int) for n in ("kind", "dtype", "M", "K", "ldx", "ldq", "n", "failed", "status")] +
+                [(n, C.c_void_p) for n in ("x", "gamma", "beta", "q", "s", "stream", "start")])
+
+
+@pytest.fixture(scope="module")
+def hammer(tmp_path_factory):
+    """A C function that makes calls from host threads at once (Python's lock would keep them apart)."""
+    if shutil.which("gcc") is None:
+        pytest.skip("no C compiler")
+    vitq.load()
+    d = tmp_path_factory.mktemp("hammer")
+    (d / "hammer.c").write_text(HAMMER)
+    subprocess.run(["gcc", "-O1", "-shared", "-fPIC", "-pthread", "-I", os.path.join(ROOT, "include"), str(d / "hammer.c"),
+                    "-o", str(d / "hammer.so"), vitq.LIB_PATH, "-Wl,-rpath," + os.path.dirname(vitq.LIB_PATH)], check=True)
+    return C.CDLL(str(d / "hammer.so")).hammer
+
+
+QUANT, LN, GELU, LN_FP8 = 0, 1, 2, 3
+# pairs of calls that run one kernel with different amounts of shared memory
+TOGETHER = {
+    "ln_1152_by_rows": [(LN, BF, 256, 1152), (LN, BF, 6256, 1152)],
+    "ln_by_width": [(LN, BF, 300, 4608), (LN, BF, 300, 16000)],
+    "ln_any_alignment": [(LN, BF, 300, 1145), (LN, BF, 3000, 1151)],
+    "quant_any_alignment": [(QUANT, BF, 40, 2101), (QUANT, BF, 40, 2303)],
+    "quant_fp32_wide": [(QUANT, F32, 20, 9301), (QUANT, F32, 20, 32767)],
+    "gelu_any_alignment": [(GELU, BF, 40, 2101), (GELU, BF, 40, 2303)],
+}
+
+
+@pytest.mark.parametrize("name", TOGETHER)
+def test_two_host_threads(name, hammer):
+    """Two threads call the same operator at different sizes, each on its own stream: no call fails, and
+    every result is the one of a call alone."""
+    jobs, keep = (Job * 2)(), []
+    for i, (kind, t, M, K) in enumerate(TOGETHER[name]):
+        x, g, b = _randn(i, M, K).to(t), (1 + 0.1 * _randn(1, K)).to(BF), (0.1 * _randn(2, K)).to(BF)
+        call = {QUANT: lambda: vitq.quant_int8(x), LN: lambda: vitq.ln_quant_int8(x, g, b), GELU: lambda: vitq.gelu_quant_int8(x),
+                LN_FP8: lambda: vitq.ln_quant(x, g, b)}[kind]
+        want, got, st = call(), [w.zero_() for w in call()], torch.cuda.Stream()
+        keep.append((x, g, b, want, got, st))
+        jobs[i] = Job(kind, vitq._DTYPES[t], M, K, K, got[1].stride(0) if kind == LN_FP8 else got[0].stride(0), 5000, 0, 0,
+                      x.data_ptr(), g.data_ptr(), b.data_ptr(), got[0].data_ptr(), got[1].data_ptr(), st.cuda_stream, None)
+    torch.cuda.synchronize()
+    failed = hammer(jobs, 2)
+    torch.cuda.synchronize()
+    assert failed == 0, f"{failed} of {sum(j.n for j in jobs)} calls failed, status {[j.status for j in jobs]}"
+    for *_, want, got, _ in keep:
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert vitq.device_error() == 0
