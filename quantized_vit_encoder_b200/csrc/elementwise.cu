@@ -665,7 +665,8 @@ static void ln_launch(const __nv_bfloat16* x, int ldx, const __nv_bfloat16* g,
   const dim3 grid((unsigned)((M + kLnRows - 1) / kLnRows)), block(16 * kLnRows);
   const size_t smem = (size_t)((K + 127) / 128) * 1536;
   auto kern = y ? ln_quant_kernel<IT, true> : ln_quant_kernel<IT, false>;
-  if (smem > 48 * 1024) cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  // the limit is the kernel's, not the launch's: the widest row's, so that a call in another thread does not lower it
+  if (smem > 48 * 1024) cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kLnMaxChunks * 1536);
   launch_pdl(kern, grid, block, smem, st, x, ldx, g, b, M, K, eps, q, s, lds, y);
 }
 

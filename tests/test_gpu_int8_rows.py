@@ -112,6 +112,7 @@ TOGETHER = {
     "quant_any_alignment": [(QUANT, BF, 40, 2101), (QUANT, BF, 40, 2303)],
     "quant_fp32_wide": [(QUANT, F32, 20, 9301), (QUANT, F32, 20, 32767)],
     "gelu_any_alignment": [(GELU, BF, 40, 2101), (GELU, BF, 40, 2303)],
+    "ln_fp8_by_width": [(LN_FP8, BF, 300, 4224), (LN_FP8, BF, 300, 4608)],
 }
 
 
