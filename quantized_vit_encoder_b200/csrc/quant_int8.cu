@@ -431,9 +431,10 @@ __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR, kRowCtas<OP, T, TPR, AN
 // Bound by issue slots (69 % busy), not by HBM (floor 13.2 us): about 25 instructions an
 // element, of which the bracket below costs 4 us, the codes 5 and the fp64 statistics 1.5.
 //
-// Statistics: exact fp64 sums of x and x^2 (bf16 -> fp64 is exact); where the mean is
-// far above the spread (E[x^2] > 2^10 var), which would cost the difference its bits,
-// the squares are summed again around the mean.
+// Statistics: exact fp64 sums of x and x^2 (bf16 -> fp64 is exact), divided by K: with the sum
+// times 1 / K instead, the mean of a constant row is one unit off that constant at one width in
+// four or so (0.2 us of 25024 x 1152).  Where the mean is far above the spread (E[x^2] > 2^10
+// var), which would cost the difference its bits, the squares are summed again around the mean.
 // y = (x - mean) rstd gamma + beta in fp32, mean as a sum of two fp32 numbers: x - mh,
 // (x - mh) r - ml r, and the last FMA round once each and r = fl32(rstd) once, so
 // |error| <= 3 2^-24 (|y| + |beta|) + 2^-24 |y| < (|y| + |beta|) 2^-21.  Where y minus and
@@ -522,7 +523,6 @@ __global__ void __launch_bounds__(TPR == 128 ? 128 : kLn8Threads, TPR == 128 ? 8
     sb[at + TPR] = make_float4(E::at(bu, 4), E::at(bu, 5), E::at(bu, 6), E::at(bu, 7));
   }
   __syncthreads();
-  const double rK = 1.0 / (double)K;
   auto sum2 = [&](double& a, double& b) {   // over the threads of a row
 #pragma unroll
     for (int o = LANES / 2; o > 0; o >>= 1) {
@@ -575,9 +575,11 @@ __global__ void __launch_bounds__(TPR == 128 ? 128 : kLn8Threads, TPR == 128 ? 8
     s1 += t1;
     s2 += t2;
     sum2(s1, s2);
-    const double mean = s1 * rK;
-    double var = fma(-mean, mean, s2 * rK);
-    const bool again = !(s2 * rK <= 1024.0 * var);   // also for a NaN
+    // one division for both: even threads have the mean, odd ones the mean square
+    const double of_k = ((t & 1) ? s2 : s1) / (double)K;
+    const double mean = __shfl_sync(0xffffffffu, of_k, 0, LANES), square = __shfl_sync(0xffffffffu, of_k, 1, LANES);
+    double var = fma(-mean, mean, square);
+    const bool again = !(square <= 1024.0 * var);   // also for a NaN
     if (TPR <= 32 ? __any_sync(0xffffffffu, again) : again) {   // the sums are the same in all threads of a row
       double d2 = 0.0, none = 0.0;
 #pragma unroll 1
@@ -590,9 +592,9 @@ __global__ void __launch_bounds__(TPR == 128 ? 128 : kLn8Threads, TPR == 128 ? 8
         }
       }
       sum2(d2, none);
-      var = d2 * rK;
+      var = d2 / (double)K;
     }
-    const double rstd = rsqrt(var + eps);
+    const double rstd = 1.0 / sqrt(var + eps);
     const float mh = (float)mean, ml = (float)(mean - (double)mh), r32 = (float)rstd;
     const bool plain = r32 >= 0x1p-100f && r32 <= 0x1p100f && fabsf(mh) <= 0x1p100f;
     const uint64_t nmh = f2pack(-mh, -mh), rr = f2pack(r32, r32), nmr = f2pack(-ml * r32, -ml * r32);

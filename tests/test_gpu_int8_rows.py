@@ -136,3 +136,32 @@ def test_two_host_threads(name, hammer):
     for *_, want, got, _ in keep:
         assert all(torch.equal(a, b) for a, b in zip(got, want))
     assert vitq.device_error() == 0
+
+
+# ------------------------------------------------------------------ LayerNorm
+# widths whose reciprocal in 64 bits times a constant row's sum is not that constant, and plain ones
+@pytest.mark.parametrize("K", [49, 103, 300, 1000, 1001, 1152, 1960, 2056, 3000, 4608, 15987, 16400])
+def test_ln_quant_constant_rows_come_out_as_beta(K):
+    values = [0.0, 1.0, 1.9921875, -1.9921875, 1.0078125, 3.140625, 1.9921875 * 2.0 ** 50, -1.9921875 * 2.0 ** 100,
+              1.9921875 * 2.0 ** 120, 1.9921875 * 2.0 ** -100]
+    x = torch.tensor(values, device="cuda").to(BF)[:, None].expand(-1, K).contiguous()
+    gamma, beta = (1 + 0.1 * _randn(1, K)).to(BF), (0.1 * _randn(2, K)).to(BF)
+    for b in (beta, torch.zeros_like(beta)):
+        for eps in (1e-6, 1.0, 1e-12):
+            _same(vitq.ln_quant_int8(x, gamma, b, eps=eps), _codes_ref(b[None].expand(len(values), K)), (K, eps))
+    q, s = vitq.ln_quant_int8(x, gamma, beta, eps=0.0)          # 0 / 0
+    assert torch.isnan(s).all() and not q.any()
+
+
+@pytest.mark.parametrize("K", [50, 98, 206, 1152, 1960, 4606, 16400])
+def test_ln_quant_results_that_are_exact_ties(K):
+    """Rows of +c and -c in turn: the mean is 0, (x - mean) rstd is +-1 exactly with eps = 0, and with
+    gamma = 1 and beta half a step of bf16 every positive result is an exact tie, which goes to even."""
+    sign = torch.ones(K, device="cuda")
+    sign[1::2] = -1
+    x = torch.stack([sign, sign * 0.5, -sign * 4096, sign * 2.0 ** -60]).to(BF)
+    gamma = torch.ones(K, dtype=BF, device="cuda")
+    for beta, up, down in ((2.0 ** -8, 1.0, -1 + 2.0 ** -8), (3 * 2.0 ** -8, 1 + 2.0 ** -6, -1 + 3 * 2.0 ** -8)):
+        y = torch.where(x.float() > 0, up, down)
+        b = torch.full((K,), beta, device="cuda").to(BF)
+        _same(vitq.ln_quant_int8(x, gamma, b, eps=0.0), _codes_ref(y), (K, beta))
