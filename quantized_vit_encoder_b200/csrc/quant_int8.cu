@@ -440,7 +440,9 @@ __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR, kRowCtas<OP, T, TPR, AN
 // |error| <= 3 2^-24 (|y| + |beta|) + 2^-24 |y| < (|y| + |beta|) 2^-21.  Where y minus and
 // plus that bound round to the same bf16 value, that value is the rounding of the exact
 // y; the other values (about 1 in 2^12) are evaluated in fp64.  Rows whose statistics are
-// not finite, or whose rstd leaves 2^-100 .. 2^100, are evaluated in fp64 as a whole.
+// not finite, whose rstd leaves 2^-100 .. 2^100, or whose mean, or mean times rstd (a constant
+// row and a tiny eps; the columns past K hold zeros and meet it), is above 2^100 are evaluated in
+// fp64 as a whole.
 
 // The bf16 results of one chunk (v: its 8 values; g, b: two float4 of gamma and of beta, the
 // second `step` behind the first): fp32 where the bracket decides, else (or where !plain) fp64.
@@ -596,7 +598,7 @@ __global__ void __launch_bounds__(TPR == 128 ? 128 : kLn8Threads, TPR == 128 ? 8
     }
     const double rstd = 1.0 / sqrt(var + eps);
     const float mh = (float)mean, ml = (float)(mean - (double)mh), r32 = (float)rstd;
-    const bool plain = r32 >= 0x1p-100f && r32 <= 0x1p100f && fabsf(mh) <= 0x1p100f;
+    const bool plain = r32 >= 0x1p-100f && r32 <= 0x1p100f && fabsf(mh) <= 0x1p100f && fabsf(mh) * r32 <= 0x1p100f;
     const uint64_t nmh = f2pack(-mh, -mh), rr = f2pack(r32, r32), nmr = f2pack(-ml * r32, -ml * r32);
     const uint64_t up = f2pack(0x1p-21f, 0x1p-21f), dn = f2pack(-0x1p-21f, -0x1p-21f);
     uint32_t m = 0u;   // bits of the largest |y|, whose bf16 rounding is the largest |bf16(y)|; a NaN is above all

@@ -165,3 +165,12 @@ def test_ln_quant_results_that_are_exact_ties(K):
         y = torch.where(x.float() > 0, up, down)
         b = torch.full((K,), beta, device="cuda").to(BF)
         _same(vitq.ln_quant_int8(x, gamma, b, eps=0.0), _codes_ref(y), (K, beta))
+
+
+@pytest.mark.parametrize("K", [40, 100, 1100, 1153, 2001, 4700])
+def test_ln_quant_constant_rows_with_a_tiny_eps(K):
+    """mean times rstd is past fp32's range, also in the columns that a thread has behind the last one."""
+    x = torch.tensor([2.0 ** 99, -2.0 ** 90, 1.0], device="cuda").to(BF)[:, None].expand(-1, K).contiguous()
+    gamma, beta = (1 + 0.1 * _randn(1, K)).to(BF), (0.1 * _randn(2, K)).to(BF)
+    for eps in (1e-20, 1e-38):
+        _same(vitq.ln_quant_int8(x, gamma, beta, eps=eps), _codes_ref(beta[None].expand(3, K)), (K, eps))
