@@ -442,7 +442,10 @@ __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR, kRowCtas<OP, T, TPR, AN
 // y; the other values (about 1 in 2^12) are evaluated in fp64.  Rows whose statistics are
 // not finite, whose rstd leaves 2^-100 .. 2^100, or whose mean, or mean times rstd (a constant
 // row and a tiny eps; the columns past K hold zeros and meet it), is above 2^100 are evaluated in
-// fp64 as a whole.
+// fp64 as a whole.  Below the normal range a rounding is off by up to 2^-150 whatever the value:
+// at most 2^-85 of y with |gamma| < 2^64 (other gammas: fp64), which the bound covers from
+// |y| = 2^-64 on.  Chunks of 8 columns below 2^-50 take fp64; a smaller value in another chunk
+// has code 0 however it is rounded.
 
 // The bf16 results of one chunk (v: its 8 values; g, b: two float4 of gamma and of beta, the
 // second `step` behind the first): fp32 where the bracket decides, else (or where !plain) fp64.
@@ -511,6 +514,7 @@ __global__ void __launch_bounds__(TPR == 128 ? 128 : kLn8Threads, TPR == 128 ? 8
   };
   if (row0 < M) fetch(row0);
   const bool wide = !ANY && ((reinterpret_cast<uintptr_t>(gamma) | reinterpret_cast<uintptr_t>(beta)) & 15u) == 0;
+  bool huge = false;   // a gamma of 2^64 or more
   for (int i = threadIdx.x; i < nc * TPR; i += blockDim.x) {   // 8 columns
     const int col = i * 8;
     uint4 gu = make_uint4(0u, 0u, 0u, 0u), bu = gu;
@@ -518,13 +522,14 @@ __global__ void __launch_bounds__(TPR == 128 ? 128 : kLn8Threads, TPR == 128 ? 8
       gu = wide ? *reinterpret_cast<const uint4*>(gamma + col) : load_chunk_edge(gamma, col, K);
       bu = wide ? *reinterpret_cast<const uint4*>(beta + col) : load_chunk_edge(beta, col, K);
     }
+    huge |= chunk_mag<__nv_bfloat16>(gu) >= 0x5F80u;
     const int at = (2 * (i / TPR)) * TPR + i % TPR;
     sg[at] = make_float4(E::at(gu, 0), E::at(gu, 1), E::at(gu, 2), E::at(gu, 3));
     sg[at + TPR] = make_float4(E::at(gu, 4), E::at(gu, 5), E::at(gu, 6), E::at(gu, 7));
     sb[at] = make_float4(E::at(bu, 0), E::at(bu, 1), E::at(bu, 2), E::at(bu, 3));
     sb[at + TPR] = make_float4(E::at(bu, 4), E::at(bu, 5), E::at(bu, 6), E::at(bu, 7));
   }
-  __syncthreads();
+  huge = __syncthreads_or(huge);
   auto sum2 = [&](double& a, double& b) {   // over the threads of a row
 #pragma unroll
     for (int o = LANES / 2; o > 0; o >>= 1) {
@@ -598,7 +603,8 @@ __global__ void __launch_bounds__(TPR == 128 ? 128 : kLn8Threads, TPR == 128 ? 8
     }
     const double rstd = 1.0 / sqrt(var + eps);
     const float mh = (float)mean, ml = (float)(mean - (double)mh), r32 = (float)rstd;
-    const bool plain = r32 >= 0x1p-100f && r32 <= 0x1p100f && fabsf(mh) <= 0x1p100f && fabsf(mh) * r32 <= 0x1p100f;
+    const bool plain =
+        !huge && r32 >= 0x1p-100f && r32 <= 0x1p100f && fabsf(mh) <= 0x1p100f && fabsf(mh) * r32 <= 0x1p100f;
     const uint64_t nmh = f2pack(-mh, -mh), rr = f2pack(r32, r32), nmr = f2pack(-ml * r32, -ml * r32);
     const uint64_t up = f2pack(0x1p-21f, 0x1p-21f), dn = f2pack(-0x1p-21f, -0x1p-21f);
     uint32_t m = 0u;   // bits of the largest |y|, whose bf16 rounding is the largest |bf16(y)|; a NaN is above all
@@ -623,8 +629,9 @@ __global__ void __launch_bounds__(TPR == 128 ? 128 : kLn8Threads, TPR == 128 ? 8
         cm = fmax3_nan(cm, fabsf(yf.x), fabsf(yf.y));   // gamma or beta may bring a NaN
       }
       uint4 w = make_uint4(h[0], h[1], h[2], h[3]);
-      if (differ) {
-        w = ln_chunk_exact(u, gp, bp, TPR, mean, rstd, plain);
+      const bool tiny = __float_as_uint(cm) - 1u < __float_as_uint(0x1p-50f) - 1u;   // 0 < cm < 2^-50
+      if (differ || tiny) {
+        w = ln_chunk_exact(u, gp, bp, TPR, mean, rstd, plain && !tiny);
         cm = E::of_mag(chunk_mag<__nv_bfloat16>(w));
       }
       // columns past K have gamma = beta = 0, so y = 0 (or NaN, in a row that has one anyway)

@@ -174,3 +174,33 @@ def test_ln_quant_constant_rows_with_a_tiny_eps(K):
     gamma, beta = (1 + 0.1 * _randn(1, K)).to(BF), (0.1 * _randn(2, K)).to(BF)
     for eps in (1e-20, 1e-38):
         _same(vitq.ln_quant_int8(x, gamma, beta, eps=eps), _codes_ref(beta[None].expand(3, K)), (K, eps))
+
+
+def _bf16_any(y):
+    """fp64 -> bf16 with one rounding, subnormal results included."""
+    step = torch.ldexp(torch.ones_like(y), torch.frexp(y)[1].clamp_min(-125) - 8)
+    return (torch.round(y / step) * step).to(F32).to(BF)
+
+
+@pytest.mark.parametrize("K", [1152, 1153, 2048, 4608])
+def test_ln_quant_results_below_the_normal_range(K):
+    """gamma so small that results are subnormal: the error of fp32 arithmetic is then absolute, not relative."""
+    M = 3000 if K < 4000 else 1000
+    x = _randn(K, M, K).to(BF)
+    for scale in (2.0 ** -130, 2.0 ** -127, 2.0 ** -120):
+        gamma = ((1 + 0.1 * _randn(1, K)).double() * scale).to(F32).to(BF)
+        c = x.double() - x.double().mean(1, keepdim=True)
+        y = c / torch.sqrt((c * c).mean(1, keepdim=True) + 1e-6) * gamma.double()
+        _same(vitq.ln_quant_int8(x, gamma, torch.zeros_like(gamma)), _codes_ref(_bf16_any(y)), (K, scale))
+
+
+@pytest.mark.parametrize("K", [1152, 4608])
+def test_ln_quant_results_of_inputs_below_the_normal_range(K):
+    """Rows of subnormal inputs under a large eps: (x - mean) rstd is subnormal, and a large gamma brings
+    the result back to the middle of the range."""
+    x = (_randn(K, 2000, K).double() * 2.0 ** -128).to(F32).to(BF)
+    for scale in (2.0 ** -4, 1.0, 2.0 ** 40, 2.0 ** 100):
+        gamma = ((1 + 0.1 * _randn(1, K)).double() * scale).to(F32).to(BF)
+        c = x.double() - x.double().mean(1, keepdim=True)
+        y = c / torch.sqrt((c * c).mean(1, keepdim=True) + 4.0) * gamma.double()
+        _same(vitq.ln_quant_int8(x, gamma, torch.zeros_like(gamma), eps=4.0), _codes_ref(_bf16_any(y)), (K, scale))
