@@ -323,7 +323,8 @@ __global__ void __launch_bounds__(16 * kLnRows, 6)
 // u << 0) and rounded to bf16.  The GELU pass is then one shared-memory lookup
 // per element followed by the block-128 quantisation.
 
-__device__ uint16_t g_gelu_table[65536];
+__device__ __align__(16) uint16_t g_gelu_table[65536];
+static_assert(__alignof__(g_gelu_table) >= 16, "read in 16-byte units");
 
 __global__ void gelu_table_kernel() {
   const int i = blockIdx.x * blockDim.x + threadIdx.x;
