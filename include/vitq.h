@@ -307,7 +307,8 @@ typedef struct {
  * of a language layer's image tokens (no counterpart in the sources for more than the two
  * axes and the layout of vit_rope2d, [FRT] s3).  Pair j of a head turns by
  * pos[axis(j)] * f_j, f_j = theta^(-j / pairs) (or per axis, see the flags); sections
- * are laid out one after the other, or interleaved.  Angles in fp64, the rest in fp32,
+ * are laid out one after the other, or interleaved.  Angles in fp64 (their sine and cosine too
+ * where the tensors are fp32), the rest in fp32,
  * one rounding.  q: [n_tokens, heads_q, head_dim], k: [n_tokens, heads_k, head_dim] by
  * the strides of p; q_out and k_out are either the inputs themselves (same pointer and
  * strides) or share no element with any input.  heads_q or heads_k may be 0 (pointers

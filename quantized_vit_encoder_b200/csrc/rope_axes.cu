@@ -16,12 +16,22 @@ constexpr int kRopeAxThreads = 256;   // wanted; one head has up to 511 items (h
 template <class T, int VEC> struct alignas(sizeof(T) * VEC) RopeVec { T v[VEC]; };
 
 // (cos, sin) of pair j of a token at pos: the angle in turns, in fp64 (a far position times a
-// frequency needs more bits than fp32 has), reduced to half a turn exactly; what is left
-// fits fp32.
+// frequency needs more bits than fp32 has), reduced to half a turn exactly.  For bf16 and fp16
+// tensors what is left is rounded to fp32 (2^-23 rad at most, against a last rounding of 2^-9 or
+// 2^-12); for fp32 tensors sine and cosine are taken in fp64 and rounded once (4096 tokens of 20
+// heads of 128: 19.0 us against 18.8, rms error 3.7e-8 against 5.4e-8 at positions about 10^5).
+template <class T>
 __device__ __forceinline__ float2 rope_cos_sin(const RopeAxes& p, int token, int j) {
   const double turn = (double)p.pos[token * p.pos_t + p.axis[j] * p.pos_a] * p.turns[j];
   float sn, cn;
-  sincospif((float)(2.0 * (turn - rint(turn))), &sn, &cn);
+  if constexpr (sizeof(T) == 4) {
+    double s64, c64;
+    sincospi(2.0 * (turn - rint(turn)), &s64, &c64);
+    sn = (float)s64;
+    cn = (float)c64;
+  } else {
+    sincospif((float)(2.0 * (turn - rint(turn))), &sn, &cn);
+  }
   return make_float2(cn, p.inverse ? -sn : sn);
 }
 
@@ -63,7 +73,7 @@ __global__ void __launch_bounds__(VEC == 1 ? 2 * kRopeAxThreads : kRopeAxThreads
   };
   for (int i = threadIdx.x; i < ntok * p.pairs; i += blockDim.x) {
     const int t = i / p.pairs, j = i - t * p.pairs;
-    cs[cs_at(t, j / VEC, j % VEC)] = rope_cos_sin(p, tok0 + t, j);
+    cs[cs_at(t, j / VEC, j % VEC)] = rope_cos_sin<T>(p, tok0 + t, j);
   }
   __syncthreads();
   const int at = threadIdx.x / per_head, c = threadIdx.x - at * per_head;

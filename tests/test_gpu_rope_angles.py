@@ -1,0 +1,40 @@
+"""The several-axis rotary of fp32 tensors: sine and cosine are fp32 roundings of the exact angle's.
+
+Tolerance: cos and sin are off by 2^-24 of themselves, vb sin and the last FMA round once each, so
+|y - want| <= 2^-24 (|va cos| + 2 |vb sin| + |want|), want itself being at most |va cos| + |vb sin|.
+The angle is pos times a frequency made by up to 128 products in fp64: off by 2^-45 of the angle.
+"""
+import pytest
+import torch
+
+from quantized_vit_encoder_b200 import vitq
+
+pytestmark = pytest.mark.gpu
+
+
+def _randn(seed, *shape):
+    return torch.randn(shape, generator=torch.Generator(device="cuda").manual_seed(seed), device="cuda")
+
+
+@pytest.mark.parametrize("adjacent", [False, True])
+@pytest.mark.parametrize("inverse", [False, True])
+@pytest.mark.parametrize("far", [0, 300, 10 ** 5])
+@pytest.mark.parametrize("sections", [(24, 20, 20), (12, 12, 12), (18, 17), (9, 10, 11, 3)])
+def test_fp32_angles(sections, far, inverse, adjacent):
+    n, pairs = 300, sum(sections)
+    g = torch.Generator(device="cuda").manual_seed(far + pairs)
+    pos = torch.randint(-far, far + 1, (n, len(sections)), generator=g, device="cuda", dtype=torch.int32)
+    x = _randn(far, n, 3, 2 * pairs)
+    x[:, 1, :pairs] = 0                                # where one product is 0, the other's angle shows
+    x[:, 2, pairs:] = 0
+    axis = [a for a, s in enumerate(sections) for _ in range(s)]
+    freq = torch.tensor([10000.0 ** (-j / pairs) for j in range(pairs)], dtype=torch.float64, device="cuda")
+    ang = (pos.double()[:, axis] * freq)[:, None]
+    c, s = torch.cos(ang), torch.sin(ang) * (-1 if inverse else 1)
+    ia, ib = (slice(0, None, 2), slice(1, None, 2)) if adjacent else (slice(0, pairs), slice(pairs, None))
+    a, b = x[..., ia].double(), x[..., ib].double()
+    y, _ = vitq.rope_axes(x, None, pos, sections, inverse=inverse, adjacent=adjacent)
+    for got, u, v in ((y[..., ia], a * c, -b * s), (y[..., ib], b * c, a * s)):
+        tol = 2.0 ** -24 * (2 * u.abs() + 3 * v.abs()) + 2.0 ** -45 * ang.abs() * (a.abs() + b.abs())
+        off = (got.double() - (u + v)).abs() - tol
+        assert (off <= 0).all(), f"{int((off > 0).sum())} of {off.numel()} off, worst {off.max().item():.3e}"
