@@ -10,7 +10,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libvitq.so")
 SOURCES = ["vitq_all.cu", "elementwise.cu", "gemm_fp8.cu", "gemm_bf16.cu", "attention.cu", "api.cu", "merger_static.cu",
-           "quant_int8.cu", "gemm_int8.cu", "rope_axes.cu", "int8_api.cu", "ptx.cuh", "internal.h"]
+           "quant_int8.cu", "gemm_int8.cu", "rope_axes.cu", "int8_api.cu", "ptx.cuh", "internal.h",
+           "int8_choose.h"]
 
 
 def nvcc_cmd(out: str = LIB, extra=()) -> list:

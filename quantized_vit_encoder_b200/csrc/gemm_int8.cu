@@ -15,12 +15,12 @@
 // half of the time.  A K block of a pair takes about 780 cycles without loads or epilogue.
 // 6256 x 1152 x 4304 with residual: 35.7 us (19.3).  243 x 2048 x 4608: 10.4.
 // 1 x 4608 x 4608: 6.0, 21 MB of weights at 3.5 TB/s.
+#include "int8_choose.h"
 #include "internal.h"
 #include "ptx.cuh"
 
 #include <cuda_fp16.h>
 
-#include <cmath>
 #include <type_traits>
 
 namespace vitq {
@@ -764,7 +764,6 @@ __global__ void __launch_bounds__(SplitCfg::THREADS, 1)
 #pragma unroll
       for (int gr = 0; gr < (BN + 63) / 64; ++gr) {
         const int c = half * (BN / 2) + gr * 32;
-        if (BN < 64 && half) break;
         uint32_t v[32];
         tmem_ld32(tmem_base + ((uint32_t)(quad * 32) << 16) + c, v);
         tmem_wait_ld();
@@ -879,53 +878,6 @@ bool i8_words(const Int8Gemm& p) {
   I8Args a{};
   i8_paths(p, p.dtype == 2 ? 4 : 2, &a);
   return !a.c_tma || (p.residual && !a.r_tma);
-}
-
-// Which kernel: the least of these estimates, in microseconds, fitted to back-to-back calls
-// on B200 (148 SMs) over 1 <= M <= 25024, 300 <= N <= 4608, 512 <= K <= 4608; nkb = K / 128.
-//  * a 128-column K block of a 128 x 64 or 128 x 128 tile takes 0.33 us whatever its width
-//    (4 MMAs of about 150 cycles; 0.40 us once the GPU is full), of a 256 x 256 pair 0.42;
-//  * the fixed part is 3.7 us for single tiles, 5.2 for pairs, 5.4 to 6.6 for clusters (which
-//    fit the GPU 74, 33 and 15 at a time for 2, 4 and 8 CTAs);
-//  * few rows: 2 us and what passes through L2, weights once per group of tokens and tokens
-//    once per group of channels, at 7.4 TB/s.
-// Measured, the kernel chosen against the next best: 1 x 4608 x 4608 6.0 us (few rows)
-// against 11.7; 48 x 4608 x 1152 6.2 (tile) against 6.2 (few rows); 128 x 1152 x 4304 8.1 (64
-// wide, 4 parts) against 8.3; 243 x 2048 x 4608 10.3 (128 wide, 4 parts) against 11.6;
-// 972 x 1152 x 1152 6.8 (tile) against 8.1 (pairs); 6256 x 1152 x 1152 12.8 (pairs) against 14.8.
-enum I8Kernel { kRows11, kRows21, kRows22, kRows41, kTile, kPairs, kSplit64x2, kSplit64x4, kSplit128x2, kSplit128x4, kSplit128x8 };
-
-I8Kernel i8_choose(int M, int N, int K, int num_sms) {
-  if (M <= 8) return kRows11;
-  const double nkb = (K + 127) / 128, nk = (double)N * K;
-  auto tiles = [&](int bm, int bn) { return (double)((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
-  I8Kernel best = kTile;
-  double least = 1e30;
-  auto offer = [&](I8Kernel k, double us) {
-    if (us < least) {
-      least = us;
-      best = k;
-    }
-  };
-  const double waves = std::ceil(tiles(128, 128) / num_sms);
-  offer(kTile, 3.7 + nkb * (waves == 1 ? 0.33 : 0.40 * waves));
-  offer(kPairs, 5.2 + nkb * 0.42 * std::ceil(tiles(256, 256) / (num_sms / 2)));
-  auto split = [&](I8Kernel k, int bn, int parts, int fit, double fixed) {
-    if (M <= 1024 && nkb >= parts && tiles(128, bn) <= fit) offer(k, fixed + 0.33 * std::ceil(nkb / parts));
-  };
-  split(kSplit64x2, 64, 2, num_sms / 2, 5.4);
-  split(kSplit64x4, 64, 4, 33, 5.6);
-  split(kSplit128x2, 128, 2, num_sms / 2, 6.6);
-  split(kSplit128x4, 128, 4, 33, 6.6);
-  split(kSplit128x8, 128, 8, 15, 6.3);
-  auto rows = [&](I8Kernel k, int tokens, int channels) {
-    offer(k, 2.0 + 1.35e-7 * (nk * ((M + tokens - 1) / tokens) + nk / channels * M));
-  };
-  if (M > 1024) return best;   // (the kernel for few rows would have too many row groups for a grid)
-  if (M > 64) rows(kRows41, 32, 16);
-  else if (M > 16 && N >= 32 * 128) rows(kRows22, 16, 32);
-  else rows(kRows21, 16, 16);
-  return best;
 }
 
 template <class T>
