@@ -277,9 +277,9 @@ int vit_gelu_quant_int8(const void* f, int M, int K, int ldf, int8_t* q, int ldq
  * A: int8 [M, lda]; W: int8 [N, ldw]; lda and ldw % 16 == 0, A and W 16-byte
  * aligned, any K <= VITQ_MAX_DIM (what lies behind column K of a row is not used).
  * sA fp32 [M]; sW fp32 [N]; bias dtype [N] or NULL; residual dtype [M, ldr] or
- * NULL (may be C itself, with ldr == ldc); C dtype [M, ldc].  Any N, ldc, ldr and
- * alignment of the type; C and residual rows that are 16-byte aligned take the fast
- * path. */
+ * NULL (may be C itself, with ldr == ldc); C dtype [M, ldc] (columns from N on are left
+ * as they were).  Any N, ldc, ldr and alignment of the type; C and residual rows that
+ * start and end on 16 bytes take the fast path. */
 int int8_gemm(const int8_t* A, int lda, const float* sA, const int8_t* W, int ldw, const float* sW, const void* bias,
               const void* residual, int ldr, void* C, int ldc, int dtype, int M, int N, int K, void* stream);
 
@@ -307,10 +307,9 @@ typedef struct {
  * of a language layer's image tokens (no counterpart in the sources for more than the two
  * axes and the layout of vit_rope2d, [FRT] s3).  Pair j of a head turns by
  * pos[axis(j)] * f_j, f_j = theta^(-j / pairs) (or per axis, see the flags); sections
- * are laid out one after the other, or interleaved.  Angles in fp64 (their sine and cosine too
- * where the tensors are fp32), the rest in fp32,
- * one rounding.  q: [n_tokens, heads_q, head_dim], k: [n_tokens, heads_k, head_dim] by
- * the strides of p; q_out and k_out are either the inputs themselves (same pointer and
+ * are laid out one after the other, or interleaved.  Angles in fp64 (their sine and cosine
+ * too where the tensors are fp32), the rest in fp32, one rounding.  q: [n_tokens, heads_q,
+ * head_dim], k: [n_tokens, heads_k, head_dim] by the strides of p; q_out and k_out are either the inputs themselves (same pointer and
  * strides) or share no element with any input.  heads_q or heads_k may be 0 (pointers
  * unused).  pos: int32, may be negative. */
 int vit_rope_axes(const vitq_rope_axes* p, const void* q, void* q_out, const void* k, void* k_out,

@@ -33,9 +33,11 @@ struct I8Args {
   const void* residual;
   void* C;
   int ldr, ldc, M, N, K;
-  // whether boxes of C leave and of the residual arrive by TMA (16-byte aligned base and row
-  // pitch); otherwise the residual is read in words of r_word bytes (4, or 2)
-  int c_tma, r_tma, r_word;
+  // whether rows of C and of the residual lie on 16 bytes (base and pitch): boxes of the residual
+  // then arrive by TMA, otherwise in words of r_word bytes (4, or 2).  c_tma: boxes of C leave by
+  // TMA.  That also takes rows that end on 16 bytes: a store writes whole 16-byte units and so up
+  // to 14 bytes behind a row that ends inside one.
+  int c_units, c_tma, r_tma, r_word;
 };
 
 // ------------------------------------------------------------------ output types
@@ -472,7 +474,8 @@ void i8_paths(const Int8Gemm& p, int es, I8Args* a) {
     const uintptr_t v = reinterpret_cast<uintptr_t>(base) | pitch;
     return v % 16 == 0 ? 16 : (v | (size_t)p.N * es) % 4 == 0 ? 4 : 2;
   };
-  a->c_tma = bytes(p.C, (size_t)p.ldc * es) == 16;
+  a->c_units = bytes(p.C, (size_t)p.ldc * es) == 16;
+  a->c_tma = a->c_units && (size_t)p.N * es % 16 == 0;
   a->r_word = p.residual ? bytes(p.residual, (size_t)p.ldr * es) : 0;
   a->r_tma = a->r_word == 16;
 }
@@ -481,7 +484,7 @@ template <int BN, bool kPair, int kCols, class T>
 cudaError_t i8_launch(const Int8Gemm& p, bool words, int num_sms, cudaStream_t st) {
   using Cfg = I8Cfg<BN, kPair, kCols>;
   constexpr int es = (int)sizeof(T);
-  I8Args a{p.sA, p.sW, p.bias, p.residual, p.C, p.ldr, p.ldc, p.M, p.N, p.K, 0, 0, 0};
+  I8Args a{p.sA, p.sW, p.bias, p.residual, p.C, p.ldr, p.ldc, p.M, p.N, p.K, 0, 0, 0, 0};
   i8_paths(p, es, &a);
   const size_t pc = (size_t)p.ldc * es, pr = (size_t)p.ldr * es;
   CUtensorMap tmA, tmB, tmC, tmR;
@@ -810,7 +813,7 @@ __global__ void __launch_bounds__(SplitCfg::THREADS, 1)
         for (int i = 0; i < 8; ++i)
           v[i] += __fmaf_rn(__fmul_rn(__int2float_rn(acc[i]), sa), sw_s[u * 8 + i], bias_s[u * 8 + i]);
         T* out = reinterpret_cast<T*>(g.C) + (size_t)row * g.ldc + n;
-        if (n + 8 <= g.N && g.c_tma) {
+        if (n + 8 <= g.N && g.c_units) {
 #pragma unroll
           for (int h = 0; h < 8 / PER; ++h) reinterpret_cast<uint4*>(out)[h] = pack16<T>(v + h * PER);
         } else {
@@ -834,7 +837,7 @@ __global__ void __launch_bounds__(SplitCfg::THREADS, 1)
 template <int BN, class T>
 cudaError_t i8_launch_split(const Int8Gemm& p, int parts, cudaStream_t st) {
   using Cfg = SplitCfg;
-  I8Args a{p.sA, p.sW, p.bias, p.residual, p.C, p.ldr, p.ldc, p.M, p.N, p.K, 0, 0, 0};
+  I8Args a{p.sA, p.sW, p.bias, p.residual, p.C, p.ldr, p.ldc, p.M, p.N, p.K, 0, 0, 0, 0};
   i8_paths(p, (int)sizeof(T), &a);
   const int a_rows = p.M < Cfg::BM ? (p.M + 7) / 8 * 8 : Cfg::BM;
   const int stage_bytes = (BN + a_rows) * Cfg::BK;
@@ -859,7 +862,7 @@ cudaError_t i8_launch_split(const Int8Gemm& p, int parts, cudaStream_t st) {
 
 template <int NT, int CT, class T>
 cudaError_t i8_launch_rows(const Int8Gemm& p, cudaStream_t st) {
-  const I8Args a{p.sA, p.sW, p.bias, p.residual, p.C, p.ldr, p.ldc, p.M, p.N, p.K, 0, 0, 0};
+  const I8Args a{p.sA, p.sW, p.bias, p.residual, p.C, p.ldr, p.ldc, p.M, p.N, p.K, 0, 0, 0, 0};
   return launch_pdl(int8_gemm_rows_kernel<NT, CT, T>, dim3((p.N + 16 * CT - 1) / (16 * CT), (p.M + 8 * NT - 1) / (8 * NT)),
                     dim3(32 * kRowsWarps), 0, st, p.A, p.lda, p.W, p.ldw, a);
 }
@@ -873,7 +876,7 @@ cudaError_t i8_pairs(const Int8Gemm& p, bool words, int num_sms, cudaStream_t st
                              : i8_launch<256, true, 128, T>(p, false, num_sms, st);
 }
 
-// Whether C or the residual has rows that TMA cannot address.
+// Whether C or the residual has rows that TMA cannot move.
 bool i8_words(const Int8Gemm& p) {
   I8Args a{};
   i8_paths(p, p.dtype == 2 ? 4 : 2, &a);

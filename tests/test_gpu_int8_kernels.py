@@ -35,7 +35,7 @@ def test_shapes_take_their_kernels(tmp_path):
     """The library's choice on a B200 (148 SMs), from the header that it is compiled from."""
     if shutil.which("g++") is None:
         pytest.skip("no C++ compiler")
-    want = [(k.split(",")[0], (m, n - off, kk)) for k, (m, n, kk) in SHAPES.items() for off in (0, 1)]
+    want = [(k.split(",")[0], (m, n - off, kk)) for k, (m, n, kk) in SHAPES.items() for off in (0, 1, 4)]
     want += [(k, s) for k, shapes in EDGES.items() for s in shapes]
     src = '#include <cstdio>\n#include "int8_choose.h"\nusing namespace vitq;\nint main() {\n' + "".join(
         f'  std::printf("%d\\n", i8_choose({m}, {n}, {k}, 148) == {kernel});\n' for kernel, (m, n, k) in want) + "}\n"
@@ -85,8 +85,9 @@ def _placed(M, N, t, pad, shift):
     return buf, buf[1:M + 1, shift:shift + N], keep
 
 
-# N, padding and start of the rows of C: whole 16-byte units, and rows that start anywhere
-PLACES = [(0, 0, 0), (0, 16, 8), (1, 0, 0), (0, 3, 1), (1, 5, 4)]
+# columns fewer, padding and start of the rows of C: whole 16-byte units, rows that start anywhere, and (1, 1, 0),
+# (1, 9, 8), (4, 4, 0): rows that start on 16 bytes and end inside a unit that holds something else
+PLACES = [(0, 0, 0), (0, 16, 8), (1, 0, 0), (0, 3, 1), (1, 1, 0), (1, 9, 8), (4, 4, 0), (1, 5, 4)]
 
 
 @gpu
