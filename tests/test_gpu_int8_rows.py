@@ -204,3 +204,48 @@ def test_ln_quant_results_of_inputs_below_the_normal_range(K):
         c = x.double() - x.double().mean(1, keepdim=True)
         y = c / torch.sqrt((c * c).mean(1, keepdim=True) + 4.0) * gamma.double()
         _same(vitq.ln_quant_int8(x, gamma, torch.zeros_like(gamma), eps=4.0), _codes_ref(_bf16_any(y)), (K, scale))
+
+
+# ------------------------------------------------------------------ widths at the limits of the kernels
+# chunks (16 bytes) of a row up to which each number of threads a row is used: the widths just below, at and
+# above, where a row fills its threads' chunks (and its shared memory, where rows start anywhere) or spills
+# over into the next kernel
+ROW_LIMITS, LN_LIMITS = (160, 288, 576, 1152, 2304, 8192), (144, 256, 2048)
+
+
+def _limit_widths(limits, per, most=65536):
+    return sorted({k for c in limits for k in (c * per - 1, c * per, c * per + 1, (c + 1) * per) if k <= most})
+
+
+def _ln_ref(x, gamma, beta):
+    c = x.double() - x.double().mean(1, keepdim=True)
+    return _bf16_any(c / torch.sqrt((c * c).mean(1, keepdim=True) + 1e-6) * gamma.double() + beta.double())
+
+
+def _gelu_ref(f):
+    x = f.double()
+    return _bf16_any(x / (1 + torch.exp(-2 * math.sqrt(2 / math.pi) * (x + 0.044715 * x ** 3))))
+
+
+@pytest.mark.parametrize("shift", [0, 1])
+@pytest.mark.parametrize("op,t,K", [("quant", t, k) for t in (BF, HF, F32) for k in _limit_widths(ROW_LIMITS, 4 if t == F32 else 8)] +
+                         [("gelu", BF, k) for k in _limit_widths(ROW_LIMITS, 8)] +
+                         [("ln", BF, k) for k in _limit_widths(LN_LIMITS, 8)])
+def test_widths_at_the_limits(op, t, K, shift):
+    """Rows of x from their storage's first element on (shift 1: one element in, so that rows start anywhere)
+    to its last; sentinels around the codes and scales."""
+    M, ldq = 9, (K + 15) // 16 * 16 + 16
+    x = torch.empty(shift + M * K, dtype=t, device="cuda")[shift:].view(M, K)
+    x.copy_(_randn(K, M, K) * torch.exp(_randn(K + 1, M, 1)))
+    codes, scales = torch.full((M + 2, ldq), 99, dtype=torch.int8, device="cuda"), torch.full((M + 2,), -1.0, device="cuda")
+    out = codes[1:M + 1, :K], scales[1:M + 1]
+    if op == "quant":
+        got, y = vitq.quant_int8(x, out=out), x
+    elif op == "gelu":
+        got, y = vitq.gelu_quant_int8(x, out=out), _gelu_ref(x)
+    else:
+        g, b = (1 + 0.1 * _randn(1, K)).to(BF), (0.1 * _randn(2, K)).to(BF)
+        got, y = vitq.ln_quant_int8(x, g, b, out=out), _ln_ref(x, g, b)
+    _same(got, _codes_ref(y), (op, t, K))
+    assert (codes[0] == 99).all() and (codes[-1] == 99).all() and (codes[:, K:] == 99).all()
+    assert scales[0] == scales[-1] == -1
