@@ -118,6 +118,9 @@ int vit_rope_axes(const vitq_rope_axes* p, const void* q, void* q_out, const voi
              VITQ_ERR_INVALID_ARG);
   const int es = elem_bytes(p->dtype);
   VITQ_CHECK(al(q, es) && al(q_out, es) && al(k, es) && al(k_out, es) && al(pos, 4), VITQ_ERR_ALIGN);
+  // an output may be its own input, not the other side's tensor
+  VITQ_CHECK(n_tokens == 0 || p->heads_q == 0 || p->heads_k == 0 || (q_out != k_out && q_out != k && k_out != q),
+             VITQ_ERR_INVALID_ARG);
 
   RopeAxes r = {};
   r.side[0] = RopeSide{q, q_out, (int)p->q_token, (int)p->q_head, (int)p->q_out_token, (int)p->q_out_head, p->heads_q};
