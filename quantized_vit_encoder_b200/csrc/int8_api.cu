@@ -118,9 +118,6 @@ int vit_rope_axes(const vitq_rope_axes* p, const void* q, void* q_out, const voi
              VITQ_ERR_INVALID_ARG);
   const int es = elem_bytes(p->dtype);
   VITQ_CHECK(al(q, es) && al(q_out, es) && al(k, es) && al(k_out, es) && al(pos, 4), VITQ_ERR_ALIGN);
-  // an output may be its own input, not the other side's tensor
-  VITQ_CHECK(n_tokens == 0 || p->heads_q == 0 || p->heads_k == 0 || (q_out != k_out && q_out != k && k_out != q),
-             VITQ_ERR_INVALID_ARG);
 
   RopeAxes r = {};
   r.side[0] = RopeSide{q, q_out, (int)p->q_token, (int)p->q_head, (int)p->q_out_token, (int)p->q_out_head, p->heads_q};
@@ -146,6 +143,9 @@ int vit_rope_axes(const vitq_rope_axes* p, const void* q, void* q_out, const voi
       for (int i = 0; i < p->sections[a]; ++i) r.axis[a + p->n_axes * i] = (uint8_t)a;
     }
   }
+  // an output may be its own input, not the other side's tensor
+  VITQ_CHECK(n_tokens == 0 || p->heads_q == 0 || p->heads_k == 0 || (q_out != k_out && q_out != k && k_out != q),
+             VITQ_ERR_INVALID_ARG);
   // frequencies in turns, each from the one before it: theta^(-1/count) steps, 2^-52 of error each
   const double turn = 0.15915494309189533577;   // 1 / (2 pi)
   if (p->flags & VITQ_ROPE_AXIS_FREQ) {
