@@ -232,3 +232,17 @@ def test_every_kernel_in_one_graph_and_on_two_streams():
                 got.append((k, vitq.int8_gemm(*o)))
     torch.cuda.synchronize()
     assert all(torch.equal(y, want[k] * 2) for k, y in got) and vitq.device_error() == 0
+
+
+@gpu
+@pytest.mark.parametrize("N", [3, 8])
+def test_most_rows(N):
+    """2^24 rows, the entry point's limit; every row is one of 1000."""
+    M, (qa, sa, qw, sw) = 1 << 24, _operands(1000, N, 16)
+    want = vitq.int8_gemm(qa, sa, qw, sw)
+    times = -(-M // 1000)
+    y = vitq.int8_gemm(qa.repeat(times, 1)[:M], sa.repeat(times)[:M], qw, sw)
+    for a in range(0, M, 1000 << 10):
+        n = min(M - a, 1000 << 10)
+        assert torch.equal(y[a:a + n], want.repeat(1024, 1)[:n]), a
+    assert vitq.device_error() == 0

@@ -249,3 +249,19 @@ def test_widths_at_the_limits(op, t, K, shift):
     _same(got, _codes_ref(y), (op, t, K))
     assert (codes[0] == 99).all() and (codes[-1] == 99).all() and (codes[:, K:] == 99).all()
     assert scales[0] == scales[-1] == -1
+
+
+@pytest.mark.parametrize("op", ["quant", "ln", "gelu"])
+@pytest.mark.parametrize("K", [8, 3])
+def test_most_rows(op, K):
+    """2^24 rows, the entry points' limit; every row is one of 1000."""
+    M, few = 1 << 24, _randn(K, 1000, K).to(BF)
+    x = few.repeat(-(-M // 1000), 1)[:M]
+    g, b = (1 + 0.1 * _randn(1, K)).to(BF), (0.1 * _randn(2, K)).to(BF)
+    call = {"quant": vitq.quant_int8, "gelu": vitq.gelu_quant_int8, "ln": lambda a: vitq.ln_quant_int8(a, g, b)}[op]
+    (q, s), (wq, ws) = call(x), call(few)
+    for a in range(0, M, 1000 << 10):
+        n = min(M - a, 1000 << 10)
+        assert torch.equal(q[a:a + n], wq.repeat(1024, 1)[:n]) and torch.equal(s[a:a + n], ws.repeat(1024)[:n]), a
+    with pytest.raises(vitq.VitqError, match="unsupported shape"):
+        call(x.new_zeros((M + 1, K)))

@@ -38,3 +38,13 @@ def test_fp32_angles(sections, far, inverse, adjacent):
         tol = 2.0 ** -24 * (2 * u.abs() + 3 * v.abs()) + 2.0 ** -45 * ang.abs() * (a.abs() + b.abs())
         off = (got.double() - (u + v)).abs() - tol
         assert (off <= 0).all(), f"{int((off > 0).sum())} of {off.numel()} off, worst {off.max().item():.3e}"
+
+
+def test_most_tokens():
+    """2^24 tokens, the entry point's limit, of one narrow head; every token is one of 1000."""
+    n, few = 1 << 24, _randn(1, 1000, 1, 8).bfloat16()
+    pos = torch.arange(1000, device="cuda", dtype=torch.int32)[:, None]
+    want, _ = vitq.rope_axes(few, None, pos, (3,))
+    times = -(-n // 1000)
+    y, _ = vitq.rope_axes(few.repeat(times, 1, 1)[:n], None, pos.repeat(times, 1)[:n], (3,))
+    assert torch.equal(y, want.repeat(times, 1, 1)[:n])
