@@ -262,7 +262,8 @@ int vit_quant_int8(const void* x, int dtype, int M, int K, int ldx, int8_t* q, i
 
 /* LayerNorm with the bf16 result quantised as in vit_quant_int8 (no counterpart in
  * the sources; the LayerNorm is vit_ln_quant's: statistics and affine step in fp64,
- * one rounding to bf16).  x: bf16 [M, ldx]; gamma, beta bf16 [K]; eps >= 0. */
+ * one rounding to bf16).  x: bf16 [M, ldx]; gamma, beta bf16 [K]; eps >= 0 (with
+ * eps = 0 a constant row is 0 / 0: s = NaN and zero codes). */
 int vit_ln_quant_int8(const void* x, int M, int K, int ldx, const void* gamma, const void* beta, float eps,
                       int8_t* q, int ldq, float* s, void* stream);
 

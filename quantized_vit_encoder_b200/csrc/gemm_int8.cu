@@ -6,15 +6,17 @@
 // whole sum stays in TMEM as exact 32-bit integers (K <= 2^16 and |code| <= 128
 // keep it below 2^31) and the scales are applied once per output, in fp32, before
 // the one rounding to T.  The sums being exact, every kernel below gives the same bits:
-//   few rows    M <= 1024   mma.sync, weights streamed once; bound by L2 / HBM bytes
+//   few rows    M <= 1024   mma.sync, weights read once for each group of 8 to 32 tokens; bound by
+//                           L2 / HBM bytes, and at one group by the rounds of K (see there)
 //   split K     M <= 1024   128 x 64 / 128 tiles, a cluster's CTAs share K; bound by latency
 //   tiles       128 x 128, one CTA each, persistent
 //   pairs       256 x 256, two CTAs each, persistent; bound by the tensor cores
+// (int8_choose.h has the choice.)
 // 25024 x 3456 x 1152 (pairs, bf16): 84 .. 87 us in short runs, 98 .. 104 under the power
 // limit, against 62 .. 64 at the measured FP8 rate (3125 TFLOP/s); the tensor pipe is busy
 // half of the time.  A K block of a pair takes about 780 cycles without loads or epilogue.
-// 6256 x 1152 x 4304 with residual: 35.7 us (19.3).  243 x 2048 x 4608: 10.4.
-// 1 x 4608 x 4608: 6.0, 21 MB of weights at 3.5 TB/s.
+// 6256 x 1152 x 4304 with residual: 35.9 us (19.8).  243 x 2048 x 4608: 10.4 (1.9).
+// 1 x 4608 x 4608: 6.0 (3.3), 21 MB of weights at 3.5 TB/s.
 #include "int8_choose.h"
 #include "internal.h"
 #include "ptx.cuh"
@@ -255,8 +257,9 @@ __device__ __noinline__ void box_store(const uint8_t* slot, uint8_t* mat, size_t
   }
 }
 
-// Epilogue warp: 32 rows (thread = row) and 64 columns, 32 columns at a time; four warps a
-// scheduler (256 columns) hide each other's latencies.  A 128-byte-wide box of C (one, or
+// Epilogue warp: 32 rows (thread = row) and Cfg::COLS columns (64, or 128 where pairs have long
+// sums), 32 columns at a time; the 16 warps of a 256-wide tile with 64 columns each, four a
+// scheduler, hide each other's latencies (8 with 128 columns: i8_pairs).  A 128-byte-wide box of C (one, or
 // two in fp32) has a slot in shared memory: the residual is brought there first (for the
 // first box while the tile's sum is still running), the finished box leaves from there.
 // kWords: C or the residual may need word-by-word rows (a kernel of its own, so that the
@@ -510,9 +513,11 @@ cudaError_t i8_launch(const Int8Gemm& p, bool words, int num_sms, cudaStream_t s
 }
 
 // ------------------------------------------------------------------ few rows
-// Up to 8 NT tokens: every weight is read once and used a few times, so what counts is
-// bytes in flight.  A CTA has 16 output channels, its 8 warps take 64-byte pieces of K in
-// turn and add up in shared memory at the end.  m16n8k32 products with the channels as
+// A CTA has 8 NT tokens and 16 CT output channels: every weight is read once for 8 NT tokens and
+// used a few times, so what counts is bytes in flight.  Its 8 warps take 64-byte pieces of K in
+// turn, U at a time, and add up in shared memory at the end.  (A round of pieces waits for the one
+// before: at K = 4608 a warp has 9 pieces and takes them 4 + 4 + 1.  1 x 4608 x 4608 takes 6.0 us,
+// the floor being 3.3.)  m16n8k32 products with the channels as
 // rows; a lane's 16 bytes of a row serve two of them (the sum over K may be taken in any
 // order as long as weights and tokens agree), so nothing passes through shared memory
 // on the way in.

@@ -8,16 +8,19 @@ namespace vitq {
 // on B200 (148 SMs) over 1 <= M <= 25024, 300 <= N <= 4608, 512 <= K <= 4608; nkb = K / 128.
 //  * a 128-column K block of a 128 x 64 or 128 x 128 tile takes 0.33 us whatever its width
 //    (4 MMAs of about 150 cycles; 0.40 us once the GPU is full), of a 256 x 256 pair 0.42;
-//  * the fixed part is 3.7 us for single tiles, 5.2 for pairs, 5.4 to 6.6 for clusters (which
-//    fit the GPU 74, 33 and 15 at a time for 2, 4 and 8 CTAs);
+//  * the fixed part is 3.7 us for single tiles, 5.2 for pairs, 5.4 to 6.6 for clusters.  Of
+//    these 74, 33 and 15 run at once with 2, 4 and 8 CTAs on this part's 148 SMs (the two last
+//    numbers are its own; on another part they would only make the choice slower);
 //  * few rows: 2 us and what passes through L2, weights once per group of tokens and tokens
 //    once per group of channels, at 7.4 TB/s.
-// Clusters and few rows are offered for M <= 1024, the range that they were fitted on; few rows
-// would take more than that only where N and K are tiny.
-// Measured, the kernel chosen against the next best: 1 x 4608 x 4608 6.0 us (few rows)
-// against 11.7; 48 x 4608 x 1152 6.2 (tile) against 6.2 (few rows); 128 x 1152 x 4304 8.1 (64
-// wide, 4 parts) against 8.3; 243 x 2048 x 4608 10.3 (128 wide, 4 parts) against 11.6;
-// 972 x 1152 x 1152 6.8 (tile) against 8.1 (pairs); 6256 x 1152 x 1152 12.8 (pairs) against 14.8.
+// Clusters and few rows are offered for M <= 1024, the range that they were fitted on.  Past it
+// tiles and pairs are not always the quickest: 2000 x 100 x 4608 takes 17.2 us in tiles and would
+// take 10.6 split (64 wide, 4 parts), 1040 x 64 x 4608 15.5 and 6.3 (few rows).
+// Measured, the kernel chosen against the next best: 48 x 4608 x 1152 6.05 us (few rows) against
+// 6.14 (tile); 128 x 1152 x 4304 8.3 (128 wide, 8 parts) against 8.0 (few rows, or 64 wide in 4
+// parts); 243 x 2048 x 4608 10.3 (128 wide, 4 parts) against 11.7 (64 wide, 2 parts);
+// 972 x 1152 x 1152 6.9 (tile) against 8.1 (pairs); 6256 x 1152 x 1152 12.6 (pairs) against 15.1
+// (tile); 6256 x 1152 x 4304 34.8 (pairs) against 48.6.
 enum I8Kernel { kRows11, kRows21, kRows22, kRows41, kTile, kPairs, kSplit64x2, kSplit64x4, kSplit128x2, kSplit128x4, kSplit128x8 };
 
 inline I8Kernel i8_choose(int M, int N, int K, int num_sms) {

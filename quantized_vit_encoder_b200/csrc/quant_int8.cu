@@ -283,7 +283,7 @@ __device__ __forceinline__ uint32_t gelu_bits(uint32_t x) { return g_gelu_table[
 // The magnitudes 2^-14 .. 16 of the GELU table as shared-memory words: GELU(x) and
 // GELU(-x) in the low and high half of word bits(x) - kGeluLo (9 KB; lanes that differ
 // only in sign read one word).  Chunks with another value (zeros, infinities, about 1 in
-// 800 of a unit normal's) take the whole table from global memory.  25024 x 4304: 70.1 us,
+// 800 of a unit normal's) take the whole table from global memory.  25024 x 4304: 70.8 us,
 // the HBM floor being 49.4; the table reads bound it (3.4 words of one bank among 32 random
 // ones: before rows were loaded ahead, shared memory was busy 83 % of 74 us, issue slots 61 %).
 constexpr uint32_t kGeluLo = 0x3880u, kGeluN = 0x900u;
@@ -332,12 +332,13 @@ __device__ __forceinline__ uint4 gelu_chunk(const uint4& u, const uint32_t* lut)
 // row; the next row's are on their way while this one's codes are stored); otherwise whole
 // 16-byte chunks.  Plain rows: one CTA for each (or 8 rows, a warp each); GELU: persistent
 // over the rows, since every CTA stages the table.  Bound by memory: 9164 x 1152 bf16
-// 4.85 us (floor 4.8; 32 MB, which stay in L2 between calls), 4608 x 4608 fp32 19.5 (16.2);
-// rows of 1153, which start anywhere, 10.9.  Rows
-// of any alignment by 28 warps an SM in fp32 (9164 x 1153: 31.7 us, by the 20 that the
-// compiler's registers leave 36.6); in 2 bytes that many spill.
+// 4.9 us (floor 4.8; 32 MB, which stay in L2 between calls), 4608 x 4608 fp32 19.5 (16.2).
+// Rows of any alignment: 9164 x 1151 bf16 11.0 us (4.8), 25024 x 4303 GELU 127 (49.4): putting
+// chunks together from units is 9 instructions an element on top of 15, at few warps (GELU: 23 %
+// of the SM's, issue slots 57 % busy).  In fp32 28 warps an SM (4608 x 4607: 31.6 us, floor 16.2,
+// by the 20 that the compiler's registers leave 36.6); in 2 bytes that many spill.
 // Whole GELU chunks (kAhead): the next row is on its way, in registers, while this one is
-// worked on, at 16 warps an SM (25024 x 4304: 70.1 us, 972 x 4304: 5.0; without it 28 warps
+// worked on, at 16 warps an SM (25024 x 4304: 70.8 us, 972 x 4304: 5.0; without it 28 warps
 // 73.8 and 7.6, 20 warps 73.2 and 5.9; with it by way of shared memory 20 warps 69.4 and 6.1; 256 threads a
 // row, 3128 x 18000: 42.1 with it, 40.1 without).
 template <int OP, int TPR, bool ANY> constexpr bool kAhead = OP == kI8Gelu && !ANY && TPR <= 128;
@@ -425,11 +426,14 @@ __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR, kRowCtas<OP, T, TPR, AN
 // thread, through the three passes over them (statistics, normalised bf16 values in place,
 // codes): the loops stay rolled and the registers few, so that 32 warps share an SM and hide
 // each other's latencies, and one kernel takes any width and alignment.  (25024 x 1152:
-// 34.3 us, 25024 x 1153: 46.5, 6256 x 4608: 46.4.  With the row held in registers, 36 a
-// thread and 20 warps an SM, 1152 columns took 33.6, but that kernel held no wider or
-// unaligned row.)  gamma and beta are staged once per CTA as fp32; persistent over the rows.
-// Bound by issue slots (69 % busy), not by HBM (floor 13.2 us): about 25 instructions an
-// element, of which the bracket below costs 4 us, the codes 5 and the fp64 statistics 1.5.
+// 34.9 us, 6256 x 4608: 48.0.  With the row held in registers, 36 a thread and 20 warps an SM,
+// 1152 columns took 33.6 when this kernel took 34.3, but that kernel held no wider or unaligned
+// row.)  gamma and beta are staged once per CTA as fp32; persistent over the rows.
+// Bound by issue slots (70 % busy), not by HBM (floor 13.2 us): about 26 instructions an
+// element, of which the bracket below costs 4 us, the codes 5 and the fp64 statistics 1.5; gamma
+// and beta are read from shared memory again for every row (four 16-byte loads for 16 bytes of x).
+// Rows of any alignment: 25024 x 1151 47.9 us, 25024 x 1153 51.2; units to chunks doubles the
+// instructions (47 an element at 1153, issue slots 74 % busy).
 //
 // Statistics: exact fp64 sums of x and x^2 (bf16 -> fp64 is exact), divided by K: with the sum
 // times 1 / K instead, the mean of a constant row is one unit off that constant at one width in

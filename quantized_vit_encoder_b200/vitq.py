@@ -529,7 +529,8 @@ def rope_axes(q, k, pos, sections, theta: float = 10000.0, interleaved: bool = F
               adjacent: bool = False, inverse: bool = False, out=None, stream=None):
     """Rotary over several position axes of q [n, hq, d] and k [n, hk, d] (k may be None; any strides, the innermost
     dense) with int32 positions pos [n, axes] and `sections` rotary pairs per axis -> (q', k'), new tensors or `out`.
-    inverse=True turns back: the gradient of the rotary.  See vit_rope_axes for the flags."""
+    inverse=True turns back: the gradient of the rotary (the call itself records no autograd graph).  See
+    vit_rope_axes for the flags."""
     dev = _device(q, "q")
     n, hq, d, qt, qh = _heads(q, "q", dev, _DTYPES)
     t = q.dtype
