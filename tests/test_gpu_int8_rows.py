@@ -50,10 +50,13 @@ HAMMER = r"""
 #include "vitq.h"
 typedef struct {
   int kind, dtype, M, K, ldx, ldq, n, failed, status;
-  const void *x, *gamma, *beta;
+  const void *x, *gamma, *beta;   /* of a product: A, W and sA */
   int8_t* q;
   float* s;
   void* stream;
+  int N, ldw;
+  const float* sW;
+  const vitq_rope_axes* rope;
   pthread_barrier_t* start;
 } job;
 static void* work(void* p) {
@@ -63,6 +66,9 @@ static void* work(void* p) {
     int r = j->kind == 0   ? vit_quant_int8(j->x, j->dtype, j->M, j->K, j->ldx, j->q, j->ldq, j->s, j->stream)
             : j->kind == 1 ? vit_ln_quant_int8(j->x, j->M, j->K, j->ldx, j->gamma, j->beta, 1e-6f, j->q, j->ldq, j->s, j->stream)
             : j->kind == 2 ? vit_gelu_quant_int8(j->x, j->M, j->K, j->ldx, j->q, j->ldq, j->s, j->stream)
+            : j->kind == 4 ? int8_gemm(j->x, j->ldx, j->beta, j->gamma, j->ldw, j->sW, 0, 0, 0, j->q, j->ldq, j->dtype, j->M, j->N,
+                                       j->K, j->stream)
+            : j->kind == 5 ? vit_rope_axes(j->rope, j->x, j->q, 0, 0, (const int32_t*)j->beta, j->M, j->stream)
                            : vit_ln_quant(j->x, j->M, j->K, j->ldx, j->gamma, j->beta, 1e-6f, (uint8_t*)j->q, j->s, j->ldq, j->stream);
     if (r) j->failed++, j->status = r;
   }
@@ -87,7 +93,8 @@ int hammer(job* jobs, int threads) {
 
 class Job(C.Structure):
     _fields_ = ([(n, C.c_int) for n in ("kind", "dtype", "M", "K", "ldx", "ldq", "n", "failed", "status")] +
-                [(n, C.c_void_p) for n in ("x", "gamma", "beta", "q", "s", "stream", "start")])
+                [(n, C.c_void_p) for n in ("x", "gamma", "beta", "q", "s", "stream")] + [("N", C.c_int), ("ldw", C.c_int)] +
+                [(n, C.c_void_p) for n in ("sW", "rope", "start")])
 
 
 @pytest.fixture(scope="module")
@@ -103,7 +110,7 @@ def hammer(tmp_path_factory):
     return C.CDLL(str(d / "hammer.so")).hammer
 
 
-QUANT, LN, GELU, LN_FP8 = 0, 1, 2, 3
+QUANT, LN, GELU, LN_FP8, GEMM, ROPE = range(6)
 # pairs of calls that run one kernel with different amounts of shared memory
 TOGETHER = {
     "ln_1152_by_rows": [(LN, BF, 256, 1152), (LN, BF, 6256, 1152)],
@@ -128,7 +135,11 @@ def test_two_host_threads(name, hammer):
         want, got, st = call(), [w.zero_() for w in call()], torch.cuda.Stream()
         keep.append((x, g, b, want, got, st))
         jobs[i] = Job(kind, vitq._DTYPES[t], M, K, K, got[1].stride(0) if kind == LN_FP8 else got[0].stride(0), 5000, 0, 0,
-                      x.data_ptr(), g.data_ptr(), b.data_ptr(), got[0].data_ptr(), got[1].data_ptr(), st.cuda_stream, None)
+                      x.data_ptr(), g.data_ptr(), b.data_ptr(), got[0].data_ptr(), got[1].data_ptr(), st.cuda_stream)
+    _hammer(hammer, jobs, keep)
+
+
+def _hammer(hammer, jobs, keep):
     torch.cuda.synchronize()
     failed = hammer(jobs, 2)
     torch.cuda.synchronize()
@@ -136,6 +147,38 @@ def test_two_host_threads(name, hammer):
     for *_, want, got, _ in keep:
         assert all(torch.equal(a, b) for a, b in zip(got, want))
     assert vitq.device_error() == 0
+
+
+# products that share a kernel (split K by 4 and 8, single tiles, pairs), or a code path
+@pytest.mark.parametrize("shapes", [((243, 2048, 4600), (121, 1104, 5001)), ((301, 4304, 1151), (972, 1152, 1152)),
+                                    ((2100, 1160, 1100), (5001, 2688, 203)), ((7, 200, 303), (30, 1160, 1000))])
+def test_two_host_threads_of_products(shapes, hammer):
+    jobs, keep = (Job * 2)(), []
+    for i, (M, N, K) in enumerate(shapes):
+        qa, sa = vitq.quant_int8(_randn(i, M, K))
+        qw, sw = vitq.quant_int8(_randn(i + 2, N, K))
+        want, st = vitq.int8_gemm(qa, sa, qw, sw), torch.cuda.Stream()
+        got = torch.zeros_like(want)
+        keep.append((qa, sa, qw, sw, (want,), (got,), st))
+        jobs[i] = Job(GEMM, vitq._DTYPES[BF], M, K, qa.stride(0), N, 3000, 0, 0, qa.data_ptr(), qw.data_ptr(), sa.data_ptr(),
+                      got.data_ptr(), None, st.cuda_stream, N, qw.stride(0), sw.data_ptr())
+    _hammer(hammer, jobs, keep)
+
+
+def test_two_host_threads_of_the_rotary(hammer):
+    jobs, keep = (Job * 2)(), []
+    for i, (n, h, sections) in enumerate(((16, 8, (12, 12, 12)), (4096, 16, (24, 20, 20)))):
+        d = 2 * sum(sections)
+        x = _randn(i, n, h, d).to(BF)
+        pos = torch.arange(3 * n, device="cuda", dtype=torch.int32).view(n, 3)
+        p = vitq.RopeAxes(vitq._DTYPES[BF], 3, (C.c_int32 * 4)(*sections, 0), h, 0, d, 0, 10000.0, h * d, d, h * d, d,
+                          0, 0, 0, 0, 3, 1)
+        want, st = vitq.rope_axes(x, None, pos, sections)[0], torch.cuda.Stream()
+        got = torch.zeros_like(want)
+        keep.append((x, pos, p, (want,), (got,), st))
+        jobs[i] = Job(ROPE, 0, n, 0, 0, 0, 3000, 0, 0, x.data_ptr(), None, pos.data_ptr(), got.data_ptr(), None, st.cuda_stream,
+                      0, 0, None, C.addressof(p))
+    _hammer(hammer, jobs, keep)
 
 
 # ------------------------------------------------------------------ LayerNorm

@@ -1,8 +1,9 @@
-"""The several-axis rotary of fp32 tensors: sine and cosine are fp32 roundings of the exact angle's.
+"""The several-axis rotary: angles of fp32 tensors, the most tokens, and what lies around the heads.
 
-Tolerance: cos and sin are off by 2^-24 of themselves, vb sin and the last FMA round once each, so
-|y - want| <= 2^-24 (|va cos| + 2 |vb sin| + |want|), want itself being at most |va cos| + |vb sin|.
-The angle is pos times a frequency made by up to 128 products in fp64: off by 2^-45 of the angle.
+Tolerance of the angles' test: cos and sin are fp32 roundings of the exact angle's, off by 2^-24 of themselves;
+vb sin and the last FMA round once each, so |y - want| <= 2^-24 (|va cos| + 2 |vb sin| + |want|), want itself
+being at most |va cos| + |vb sin|.  The angle is pos times a frequency made by up to 128 products in fp64: off by
+2^-45 of the angle.
 """
 import pytest
 import torch
@@ -48,3 +49,29 @@ def test_most_tokens():
     times = -(-n // 1000)
     y, _ = vitq.rope_axes(few.repeat(times, 1, 1)[:n], None, pos.repeat(times, 1)[:n], (3,))
     assert torch.equal(y, want.repeat(times, 1, 1)[:n])
+
+
+@pytest.mark.parametrize("t", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("adjacent", [False, True])
+@pytest.mark.parametrize("sections,d,gap", [((24, 20, 20), 128, 8), ((24, 20, 20), 144, 16), ((12, 12, 12), 72, 4),
+                                            ((12, 12, 12), 84, 4), ((9, 9), 40, 2), ((5,), 11, 1), ((5,), 10, 3)])
+def test_nothing_around_the_heads_is_written(sections, d, gap, adjacent, t):
+    """Heads of q and k between sentinels, at each width of access, out of place and in place."""
+    n, hq, hk = 37, 3, 2
+    row = (hq + hk) * (d + gap) + gap
+    x = torch.full((n, row), 7.0, device="cuda").to(t)
+    q = x.as_strided((n, hq, d), (row, d + gap, 1), gap)
+    k = x.as_strided((n, hk, d), (row, d + gap, 1), gap + hq * (d + gap))
+    q.copy_(_randn(1, n, hq, d))
+    k.copy_(_randn(2, n, hk, d))
+    pos = torch.arange(n * len(sections), device="cuda", dtype=torch.int32).view(n, len(sections))
+    want = vitq.rope_axes(q.contiguous(), k.contiguous(), pos, sections, adjacent=adjacent)
+    before, inside = x.clone(), torch.zeros(n, row, dtype=torch.bool, device="cuda")
+    for v in (q, k):
+        inside.as_strided(v.shape, v.stride(), v.storage_offset()).fill_(True)
+    out = torch.full_like(x, 5.0)
+    oq, ok = (out.as_strided(v.shape, v.stride(), v.storage_offset()) for v in (q, k))
+    vitq.rope_axes(q, k, pos, sections, adjacent=adjacent, out=(oq, ok))
+    assert torch.equal(oq, want[0]) and torch.equal(ok, want[1]) and (out[~inside] == 5.0).all() and torch.equal(x, before)
+    vitq.rope_axes_(q, k, pos, sections, adjacent=adjacent)
+    assert torch.equal(q, want[0]) and torch.equal(k, want[1]) and torch.equal(x[~inside], before[~inside])
