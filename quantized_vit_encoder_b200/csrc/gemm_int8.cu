@@ -749,11 +749,13 @@ __global__ void __launch_bounds__(SplitCfg::THREADS, 1)
       bias_s[c] = g.bias && n < g.N ? to_f32<T>(reinterpret_cast<const T*>(g.bias)[n]) : 0.f;
     }
     if (row_in) sa = g.sA[row];
+    // no residual: -0, which leaves any sum as it is (a product that underflows to -0 too)
+    constexpr uint32_t none = sizeof(T) == 4 ? 0x80000000u : 0x80008000u;
 #pragma unroll
     for (int k = 0; k < UNITS; ++k) {
       const int u = half + 2 * k, n = n0 + c_first + u * 8;
 #pragma unroll
-      for (int h = 0; h < 8 / PER; ++h) ru[k][h] = make_uint4(0u, 0u, 0u, 0u);
+      for (int h = 0; h < 8 / PER; ++h) ru[k][h] = make_uint4(none, none, none, none);
       if (g.residual && row_in && u < cols / 8 && n < g.N) {
         const T* res = reinterpret_cast<const T*>(g.residual) + (size_t)row * g.ldr + n;
         if (n + 8 <= g.N && g.r_tma) {

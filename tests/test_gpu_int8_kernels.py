@@ -206,6 +206,18 @@ def test_row_does_not_depend_on_the_kernel():
 
 
 @gpu
+@pytest.mark.parametrize("t", [BF, F32])
+def test_products_that_underflow_have_the_same_sign_in_every_kernel(t):
+    """Below 2^-150 a product becomes a zero of its sign."""
+    for kernel in ("kSplit64x4", "kSplit128x4", "kTile", "kPairs", "kRows41"):
+        M, N, K = SHAPES[kernel]
+        qa, sa, qw, sw = _operands(M, N, K)
+        y = vitq.int8_gemm(qa, sa * 1e-26, qw, sw * 1e-26, out_dtype=t)
+        few = vitq.int8_gemm(qa[:5], sa[:5] * 1e-26, qw, sw * 1e-26, out_dtype=t)
+        assert not y.any() and torch.signbit(y).any() and torch.equal(torch.signbit(y[:5]), torch.signbit(few)), kernel
+
+
+@gpu
 def test_every_kernel_in_one_graph_and_on_two_streams():
     ops = {k: _operands(*s) for k, s in SHAPES.items()}
     want = {k: vitq.int8_gemm(*o) for k, o in ops.items()}
